@@ -255,7 +255,8 @@ MOE_API int moe_launches_per_call(const moe_shape_t* shape, int device, int* lau
  * status word [2] and returns early instead of trapping.  Test knob:
  * MOE_TEST_WITHHOLD_FLAG=n (read once per process) makes the first n
  * single-launch calls leave one mid flag unpublished, so that those waits run
- * out and the call reports MOE_ERR_DEVICE_TIMEOUT; the next call is normal.  */
+ * out and the call reports MOE_ERR_DEVICE_TIMEOUT; the next call is normal.
+ * moe_linear_w4 counts as such a call (it withholds one part of a sum).     */
 MOE_API int moe_get_status(void* workspace, void* stream, int32_t* device_status);
 
 /* Size of the scratch array behind moe_forward_static (8 MiB).            */
@@ -330,6 +331,48 @@ MOE_API int moe_pack_mxfp4_scales(const uint8_t* scales, int64_t batch, int32_t 
  * round-to-nearest-even, saturating.  scales: [batch][rows/128][K/128].    */
 MOE_API int moe_quantize_fp8_block128(const float* w, int64_t batch, int32_t rows,
                               int32_t K, uint8_t* q, float* scales, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Few-token operators: MXFP4 weights with bf16 activations (nothing but the
+ * weights is quantized; the calls above quantize the activations too).  Sums
+ * are fp32.  An infinity or a NaN in a token's row makes that token's outputs
+ * NaN and leaves the other tokens' alone; a subnormal activation (below 2^-126)
+ * counts as zero.  Results do not depend on timing:
+ * the same call gives the same bits.                                        */
+
+enum { MOE_OUT_BF16 = 0, MOE_OUT_F32 = 1 };
+
+/* out[m][n] = sum_k x[m][k] * W[n][k] (+ bias[n]).  M >= 1 tokens (meant for a
+ * few; any number works), N >= 1 rows of weights, K % 32 == 0.
+ *   ldx, ldo   elements between rows of x and of out (ldx >= K, ldx % 8 == 0;
+ *              ldo >= N); columns past K and N are neither read nor written
+ *   out_type   MOE_OUT_BF16 (rounded once) or MOE_OUT_F32                    */
+typedef struct {
+  int32_t M, N, K, out_type;
+  int64_t ldx, ldo;
+} moe_linear_shape_t;
+
+/* Bytes of an [N][K] MXFP4 matrix in the layout moe_linear_w4 reads.       */
+MOE_API int moe_w4_packed_size(int32_t N, int32_t K, size_t* bytes);
+
+/* MXFP4 as moe_quantize_mxfp4 writes it (codes q [N][K/2], scales [N][K/32])
+ * into moe_linear_w4's layout, once, offline: blocks of 128 rows x 128 K, a
+ * block's codes (8192 bytes, rows of 64) contiguous, [ceil(N/128)][ceil(K/128)]
+ * of them, followed by as many 512-byte scale blocks in the order of
+ * moe_pack_mxfp4_scales; missing rows and columns are zero.  q 16-byte,
+ * packed 256-byte aligned, packed of moe_w4_packed_size bytes, no overlap.  */
+MOE_API int moe_pack_w4(const uint8_t* q, const uint8_t* scales, int32_t N, int32_t K, uint8_t* packed, void* stream);
+
+/* Workspace bytes of moe_linear_w4 (host only, pure).                       */
+MOE_API int moe_linear_w4_workspace_size(const moe_linear_shape_t* shape, size_t* bytes);
+
+/* The product.  x bf16, 16-byte aligned; w_packed from moe_pack_w4; bias fp32
+ * [N] or NULL; out must not overlap an input.  The workspace is zero-filled
+ * once (moe_workspace_init) and then serves any sequence of moe_linear_w4
+ * calls on one stream, of any shapes it is large enough for; moe_get_status
+ * reports a device-side wait that ran out (zero-fill the workspace then).   */
+MOE_API int moe_linear_w4(const moe_linear_shape_t* shape, const void* x, const void* w_packed, const float* bias,
+                          void* out, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,8 @@ __all__ = [
     "MOE_W_MXFP4", "MOE_W_FP8_BLOCK128", "MoeError", "MoeShape", "library_path", "load",
     "moe_last_error", "moe_workspace_size", "moe_workspace_layout", "moe_workspace_init", "moe_route",
     "moe_forward", "moe_forward_routed", "moe_forward_partial", "moe_round_bf16", "moe_forward_timed", "moe_forward_static", "moe_get_status_static", "moe_launches_per_call", "MOE_STATIC_SCRATCH_BYTES", "moe_get_status", "moe_quantize_mxfp4", "moe_pack_mxfp4_scales", "moe_quantize_fp8_block128",
+    "MOE_OUT_BF16", "MOE_OUT_F32", "MoeLinearShape", "moe_w4_packed_size", "moe_pack_w4",
+    "moe_linear_w4_workspace_size", "moe_linear_w4",
     "moe_probe_tensor_peak", "MOE_PROBE_FP8", "MOE_PROBE_FP4", "MOE_PROBE_BF16",
 ]
 
@@ -31,6 +33,8 @@ MOE_ERR_CUDA = -5
 MOE_ERR_DEVICE_TIMEOUT = -6
 MOE_W_MXFP4 = 1
 MOE_W_FP8_BLOCK128 = 2
+MOE_OUT_BF16 = 0
+MOE_OUT_F32 = 1
 MOE_PROBE_FP8 = 0
 MOE_PROBE_FP4 = 1
 MOE_PROBE_BF16 = 2
@@ -58,6 +62,16 @@ class MoeShape(ctypes.Structure):
     @classmethod
     def of(cls, M, H, I, E, topk, routed_scale, wfmt):
         return cls(M, H, I, E, topk, routed_scale, wfmt)
+
+
+class MoeLinearShape(ctypes.Structure):
+    """Shape of moe_linear_w4; a program that repeats a call keeps one."""
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("out_type", ctypes.c_int32),
+                ("ldx", ctypes.c_int64), ("ldo", ctypes.c_int64)]
+
+    @classmethod
+    def of(cls, M, N, K, ldx=None, ldo=None, out_type=MOE_OUT_BF16):
+        return cls(M, N, K, out_type, K if ldx is None else ldx, N if ldo is None else ldo)
 
 
 class _Layout(ctypes.Structure):
@@ -97,6 +111,10 @@ def load():
         "moe_quantize_mxfp4": [P, I64, I32, P, P, P],
         "moe_pack_mxfp4_scales": [P, I64, I32, I32, P, P],
         "moe_quantize_fp8_block128": [P, I64, I32, I32, P, P, P],
+        "moe_w4_packed_size": [I32, I32, ctypes.POINTER(SZ)],
+        "moe_pack_w4": [P, P, I32, I32, P, P],
+        "moe_linear_w4_workspace_size": [ctypes.POINTER(MoeLinearShape), ctypes.POINTER(SZ)],
+        "moe_linear_w4": [ctypes.POINTER(MoeLinearShape), P, P, P, P, P, SZ, P],
         "moe_probe_tensor_peak": [I32, I32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double), P],
     }
     for name, args in sig.items():
@@ -118,9 +136,12 @@ def _ptr(t):
 
 
 def _stream(s):
-    if s is None:
+    if s is None:   # torch's current stream; the raw query costs 0.2 us, torch.cuda.current_stream() 3 us
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        try:
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:
+            return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -265,3 +286,29 @@ def moe_quantize_fp8_block128(w, batch: int, rows: int, K: int, q, scales, strea
                               check: bool = True) -> int:
     rc = load().moe_quantize_fp8_block128(_ptr(w), batch, rows, K, _ptr(q), _ptr(scales), _stream(stream))
     return _ret(rc, "moe_quantize_fp8_block128", check)
+
+
+def moe_w4_packed_size(N: int, K: int) -> int:
+    """Bytes of an [N][K] MXFP4 matrix in moe_linear_w4's layout."""
+    n = ctypes.c_size_t(0)
+    _ret(load().moe_w4_packed_size(N, K, ctypes.byref(n)), "moe_w4_packed_size", True)
+    return n.value
+
+
+def moe_pack_w4(q, scales, N: int, K: int, packed, stream=None, check: bool = True) -> int:
+    """MXFP4 codes [N][K/2] and scales [N][K/32] -> moe_linear_w4's layout (include/moe_b200.h)."""
+    return _ret(load().moe_pack_w4(_ptr(q), _ptr(scales), N, K, _ptr(packed), _stream(stream)), "moe_pack_w4", check)
+
+
+def moe_linear_w4_workspace_size(shape: MoeLinearShape) -> int:
+    n = ctypes.c_size_t(0)
+    _ret(load().moe_linear_w4_workspace_size(ctypes.byref(shape), ctypes.byref(n)), "moe_linear_w4_workspace_size", True)
+    return n.value
+
+
+def moe_linear_w4(shape: MoeLinearShape, x, w_packed, bias, out, workspace, ws_bytes: int, stream=None,
+                  check: bool = True) -> int:
+    """out = x W^T (+ bias) for few tokens: MXFP4 weights, bf16 activations kept as they are, fp32 sums."""
+    rc = load().moe_linear_w4(ctypes.byref(shape), _ptr(x), _ptr(w_packed), _ptr(bias), _ptr(out), _ptr(workspace),
+                              ws_bytes, _stream(stream))
+    return _ret(rc, "moe_linear_w4", check)

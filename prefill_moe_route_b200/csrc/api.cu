@@ -16,7 +16,7 @@
 #include <atomic>
 #include <mutex>
 
-#include "internal.h"
+#include "host.h"
 
 namespace moe {
 
@@ -39,12 +39,10 @@ int small_cluster_size();
 cudaError_t launch_small(const CUtensorMap& w13, const CUtensorMap& w2, const CUtensorMap& mid,
                          const SmallParams& p, int nclusters, cudaStream_t st);
 
-static size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
 // Text of the last failure on this thread (moe_last_error).
 static thread_local char g_last_error[256] = "";
 
-static int fail(int code, const char* what, cudaError_t e = cudaSuccess) {
+int fail(int code, const char* what, cudaError_t e) {
   if (e != cudaSuccess)
     std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s", what, cudaGetErrorString(e));
   else
@@ -158,7 +156,7 @@ static EncodeTiledFn encode_fn() {
   return fn;
 }
 
-static bool make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const uint64_t* dims,
+bool make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const uint64_t* dims,
                      const uint64_t* strides_bytes, const uint32_t* box) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
@@ -172,7 +170,7 @@ static bool make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const voi
   return r == CUDA_SUCCESS;
 }
 
-static int sm_count(int dev) {
+int sm_count(int dev) {
   static int cache[64] = {0};
   if (dev < 0 || dev >= 64) return 148;
   if (!cache[dev]) {
@@ -183,7 +181,7 @@ static int sm_count(int dev) {
   return cache[dev];
 }
 
-static uint64_t wait_timeout_ns() {
+uint64_t wait_timeout_ns() {
   static uint64_t v = [] {
     const char* e = std::getenv("MOE_WAIT_TIMEOUT_MS");
     long ms = e ? std::atol(e) : 2000;
@@ -198,7 +196,7 @@ static uint64_t wait_timeout_ns() {
 // run out (bounded by MOE_WAIT_TIMEOUT_MS) and the call reports
 // MOE_ERR_DEVICE_TIMEOUT through the status word.  Read once per process.
 static std::atomic<int> g_withhold_left{-1};
-static int take_withhold() {
+int take_withhold() {
   int left = g_withhold_left.load();
   if (left < 0) {
     const char* e = std::getenv("MOE_TEST_WITHHOLD_FLAG");
@@ -219,22 +217,10 @@ static int device_of(const void* ptr) {
   return a.device;
 }
 
-struct DeviceGuard {
-  int prev = -1;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    if (prev != dev) cudaSetDevice(dev);
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-  }
-};
-
 // Device of the stream, checked against every pointer; <0 is an error code.
 // Pointer attributes are not queried while the stream is being captured into
 // a CUDA graph (the eager calls before capture check the same buffers).
-static int resolve_device(void* stream, const void* const* ptrs, int n) {
+int resolve_device(void* stream, const void* const* ptrs, int n) {
   int dev = -1;
   cudaError_t e;
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
@@ -259,8 +245,6 @@ static int resolve_device(void* stream, const void* const* ptrs, int n) {
   }
   return dev;
 }
-
-static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Scratch of moe_forward_static, for callers that cannot allocate device
 // memory: one fixed array per device that loads the library, held until the

@@ -143,4 +143,21 @@ struct CombineParams {
   int M, H, topk;
 };
 
+// Parameters of the few-token product y = x W^T on MXFP4 weights (linear.cu).
+struct LinearParams {
+  const uint16_t* x;        // bf16, rows ldx elements apart
+  const float* bias;        // may be null
+  const uint8_t* wsf;       // packed weight scales: 512-byte blocks [N/128][K/128]
+  uint8_t* xop;             // above 16 tokens: operand blocks and scale blocks [token tile][K/128]
+  uint8_t* xsf;
+  void* out;                // rows ldo elements apart
+  uint32_t* part;           // [grid][tokens per tile][128] parts of tiles cut between shares, zero between calls
+  int32_t* status;
+  int64_t ldx, ldo, units;  // units = row tiles x token tiles x KU
+  int M, N, K, KC, KU, TT;  // K chunks of 128, units along K, token tiles
+  int out_f32;
+  int test_withhold;        // test knob: leave the last share's part unpublished
+  uint64_t timeout_ns;
+};
+
 }  // namespace moe

@@ -1,0 +1,486 @@
+// linear.cu -- y = x W^T (+ bias) for few tokens: MXFP4 weights, bf16
+// activations, fp32 sums, one launch.
+//
+// Bound: the weights' bytes.  The product runs on the tensor cores with the
+// weights on the MMA's M side straight from their packed 4-bit form (no
+// dequantization) and the tokens as 2 columns each (w4.cuh).  The K-chunks of
+// all row tiles are one sequence of units (128 rows x 256 K, 17 KB) that the
+// CTAs, one per SM, share evenly: every SM streams the same bytes whatever the
+// shape.  Where a tile is cut between shares, the share that starts it adds the
+// others' parts in K order (so results do not depend on timing); those are the
+// first thing that their CTAs finish, and the starting share's last.
+//
+// Roles: one thread streams tiles (TMA) and their scale blocks (bulk copy),
+// eight warps split the tokens' K chunks into the operand ring, one thread
+// issues the MMAs, four warps read the sums out of TMEM.
+#include <atomic>
+
+#include "w4.cuh"
+
+namespace moe {
+namespace linear {
+
+using namespace w4;
+
+constexpr int SPLIT_WARPS = 8;
+constexpr int MAX_GROUPS = 4;       // units whose operand is being split at once
+constexpr int WARP_SPLIT0 = 2;
+constexpr int UK = 2;               // K chunks of 128 in a unit
+constexpr int SF_SLOTS = 4;         // TMEM scale slots: per chunk 4 columns of weight scales + 4 of token scales
+
+template <int NC>
+struct Cfg {                        // NC: operand columns, two per token
+  static constexpr int MT = NC / 2;
+  // Above 16 tokens every CTA splitting its own K chunks costs more than one
+  // small kernel that does it once (k_split_x) and a bulk copy per unit.
+  static constexpr bool PRE = NC >= 64;
+  static constexpr int WARP_EPI0 = WARP_SPLIT0 + (PRE ? 2 : SPLIT_WARPS);   // the two are idle: TMEM quarters
+  static constexpr int THREADS = (WARP_EPI0 + 4) * 32;
+  static constexpr int B_TILE = NC * 128;
+  static constexpr int A_BYTES = UK * A_TILE, B_BYTES = UK * B_TILE, SF_BYTES = UK * SF_BLOCK;
+  static constexpr int STAGE = A_BYTES + B_BYTES + 2 * SF_BYTES;   // weights, tokens, their scales
+  static constexpr int STAGES = NC >= 128 ? 3 : NC >= 64 ? 4 : 5;
+  static constexpr int TMEM_COLS = NC >= 128 ? 512 : 256;
+  static constexpr int SF_COL0 = 2 * NC;
+  // a group of split warps two rounds ahead of the MMA would read a slot's old phase
+  static_assert(PRE || MAX_GROUPS <= STAGES, "ring depth");
+};
+
+struct Smem {
+  uint64_t full[8], empty[8], accf[2], acce[2];
+  uint32_t tmem;
+  int abort_flag;
+};
+
+template <int NC>
+constexpr int smem_bytes() {
+  return Cfg<NC>::STAGES * Cfg<NC>::STAGE + (int)sizeof(Smem) + 1024;
+}
+static_assert(smem_bytes<16>() <= 232448 && smem_bytes<32>() <= 232448 && smem_bytes<64>() <= 232448 &&
+                  smem_bytes<128>() <= 232448, "shared memory");
+
+// 8 values of JB tokens' K chunk each: 8 bf16 in, 8 bytes of both operand
+// columns out; four neighbouring lanes hold a block of 32.  The JB chains run
+// side by side: one alone is a few hundred clocks of dependent conversions.
+template <int JB>
+__device__ __forceinline__ void split_items(const uint4* u, uint8_t* tile, uint8_t* sf, int n0, int step, int mt, int g8) {
+  uint32_t w[JB][4], am[JB];
+#pragma unroll
+  for (int j = 0; j < JB; ++j) {
+    w[j][0] = u[j].x; w[j][1] = u[j].y; w[j][2] = u[j].z; w[j][3] = u[j].w;
+    uint32_t a = 0;   // largest magnitudes as bf16 bits
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a = max_u16x2(a, w[j][i] & 0x7FFF7FFFu);
+    am[j] = max(a & 0xFFFFu, a >> 16);
+  }
+#pragma unroll
+  for (int j = 0; j < JB; ++j) am[j] = max(am[j], __shfl_xor_sync(0xFFFFFFFFu, am[j], 1));
+#pragma unroll
+  for (int j = 0; j < JB; ++j) am[j] = max(am[j], __shfl_xor_sync(0xFFFFFFFFu, am[j], 2));
+  uint32_t hi[JB][4], lo[JB][4];
+  int s[JB];
+#pragma unroll
+  for (int j = 0; j < JB; ++j) {
+    s[j] = split_exp(__uint_as_float(am[j] << 16));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      split_f16x2(s[j] == SPLIT_NAN ? 0x7E007E00u : f16x2_scaled(w[j][i], s[j]), hi[j][i], lo[j][i]);
+  }
+#pragma unroll
+  for (int j = 0; j < JB; ++j) {
+    const int n = n0 + j * step;
+    *reinterpret_cast<uint2*>(tile + tile_byte(n, g8 * 8)) =
+        make_uint2(hi[j][0] | hi[j][1] << 16, hi[j][2] | hi[j][3] << 16);
+    *reinterpret_cast<uint2*>(tile + tile_byte(mt + n, g8 * 8)) =
+        make_uint2(lo[j][0] | lo[j][1] << 16, lo[j][2] | lo[j][3] << 16);
+    if ((g8 & 3) == 0) {
+      sf[sf_byte(n, g8 >> 2)] = static_cast<uint8_t>(split_code_hi(s[j]));
+      sf[sf_byte(mt + n, g8 >> 2)] = static_cast<uint8_t>(split_code_lo(s[j]));
+    }
+  }
+}
+
+template <int NC>
+__global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
+k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
+  using C = Cfg<NC>;
+  constexpr int MT = C::MT, WARP_EPI0 = C::WARP_EPI0;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* abuf = base;                                   // [STAGES][A_BYTES]
+  uint8_t* bbuf = abuf + C::STAGES * C::A_BYTES;          // [STAGES][B_BYTES]
+  uint8_t* asf = bbuf + C::STAGES * C::B_BYTES;           // [STAGES][SF_BYTES]
+  uint8_t* bsf = asf + C::STAGES * C::SF_BYTES;           // [STAGES][SF_BYTES]
+  Smem& S = *reinterpret_cast<Smem*>(bsf + C::STAGES * C::SF_BYTES);
+  volatile int* abort_flag = &S.abort_flag;
+
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int G = gridDim.x;
+  const int share = G - 1 - blockIdx.x;   // a share waits for later ones only, which blocks launched before it hold
+  const int KU = p.KU, TT = p.TT;
+  const int64_t U = p.units;
+  const int64_t u0 = share_begin(U, G, share), u1 = share_begin(U, G, share + 1);
+  // warps that share one unit's split: a warp for a token, as a power of two
+  const int mtile = min(p.M, MT);
+  const int gw = mtile <= 2 ? SPLIT_WARPS / MAX_GROUPS : mtile <= 4 ? 4 : 8;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) { mbar_init(&S.full[s], C::PRE ? 1 : 1 + gw); mbar_init(&S.empty[s], 1); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&S.accf[b], 1); mbar_init(&S.acce[b], 4); }
+    S.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 32) tma_prefetch_desc(&tmW);
+  if (warp == WARP_EPI0) { tmem_alloc(&S.tmem, C::TMEM_COLS); tmem_relinquish(); }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // Nothing above touches global memory.  With the operand made by k_split_x,
+  // which starts this kernel only after its own wait, everything but that
+  // operand is already there: only its reader waits.
+  if (!C::PRE) pdl_wait();
+  pdl_launch_dependents();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, S.tmem, 0);
+  const uint64_t deadline = globaltimer() + p.timeout_ns;
+  auto fail = [&](int site) {
+    *abort_flag = 1;
+    atomicOr(p.status, ST_TIMEOUT);
+    atomicCAS(p.status + 2, 0, (int)(0x80000000u | (8u << 24) | ((unsigned)site << 20) | (blockIdx.x & 0xFFFu)));
+  };
+  auto drain = [&]() { const uint64_t until = globaltimer() + 2000000ull; while (globaltimer() < until) { } };
+
+  if (warp == 0) {
+    // ------------------------------------------------ weights, their scales, ready-made operands
+    if (lane == 0) {
+      int st = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      const int64_t tile0 = u0 / KU;
+      const int ku0 = static_cast<int>(u0 - tile0 * KU), nu = static_cast<int>(u1 - u0);
+      const int rt0 = static_cast<int>(tile0 / TT), tt0 = static_cast<int>(tile0 - (int64_t)rt0 * TT);
+      auto next = [&](int& rt, int& tt, int& ku) {
+        if (++ku == KU) { ku = 0; if (++tt == TT) { tt = 0; ++rt; } }
+      };
+      auto weights = [&](int s, int rt, int ku) {
+        const int64_t blk = (int64_t)rt * p.KC + ku * UK;
+        const int nk = min(UK, p.KC - ku * UK);
+        // 4-bit tiles land unpacked.  A box holds UK chunks; a tile's odd last
+        // chunk brings its neighbour's first along (zeros past the matrix).
+        mbar_arrive_expect_tx(&S.full[s], UK * CODE_BLOCK + nk * (SF_BLOCK + (C::PRE ? C::B_TILE + SF_BLOCK : 0)));
+        tma_load_2d(abuf + s * C::A_BYTES, &tmW, &S.full[s], 0, static_cast<int>(blk * 128));
+        bulk_load(asf + s * C::SF_BYTES, p.wsf + blk * SF_BLOCK, nk * SF_BLOCK, &S.full[s]);
+      };
+      auto operand = [&](int s, int tt, int ku) {
+        const int64_t blk = (int64_t)tt * p.KC + ku * UK;
+        const int nk = min(UK, p.KC - ku * UK);
+        bulk_load(bbuf + s * C::B_BYTES, p.xop + blk * C::B_TILE, nk * C::B_TILE, &S.full[s]);
+        bulk_load(bsf + s * C::SF_BYTES, p.xsf + blk * SF_BLOCK, nk * SF_BLOCK, &S.full[s]);
+      };
+      int rt = rt0, tt = tt0, ku = ku0, i = 0;
+      if (C::PRE) {   // the ring's first round: weights, then the wait for the operand
+        for (; i < min(nu, C::STAGES); ++i) { weights(i, rt, ku); next(rt, tt, ku); }
+        pdl_wait();
+        int rt2 = rt0, tt2 = tt0, ku2 = ku0;
+        for (int j = 0; j < i; ++j) { operand(j, tt2, ku2); next(rt2, tt2, ku2); }
+        if (i == C::STAGES) ph = 1;
+        else st = i;
+      }
+      for (; i < nu; ++i) {
+        if (!mbar_wait(&S.empty[st], ph ^ 1, deadline, abort_flag)) { fail(1); ok = false; break; }
+        weights(st, rt, ku);
+        if (C::PRE) operand(st, tt, ku);
+        if (++st == C::STAGES) { st = 0; ph ^= 1; }
+        next(rt, tt, ku);
+      }
+      if (!ok) drain();
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer (the whole warp, one lane issues)
+    constexpr uint32_t IDESC = idesc_block_scaled(FMT8_E2M1, FMT8_E4M3, NC);
+    int st = 0, slot = 0, seg = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    int ku = static_cast<int>(u0 % KU);
+    bool first = true;
+    const int nu = static_cast<int>(u1 - u0);
+    for (int i = 0; i < nu; ++i) {
+      const int b = seg & 1;
+      if (first && !mbar_wait(&S.acce[b], ((seg >> 1) & 1) ^ 1, deadline, abort_flag)) { fail(2); ok = false; break; }
+      if (!mbar_wait(&S.full[st], ph, deadline, abort_flag)) { fail(3); ok = false; break; }
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t d = tmem + b * NC;
+      const int nk = min(UK, p.KC - ku * UK);
+      const bool last = ku + 1 == KU || i + 1 == nu;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < UK; ++kk) {
+          if (kk >= nk) break;
+          const uint32_t sfa = tmem + C::SF_COL0 + ((slot + kk) % SF_SLOTS) * 8, sfb = sfa + 4;
+          tc_cp_sf(sfa, sdesc_sf(smem_u32(asf + st * C::SF_BYTES + kk * SF_BLOCK)));
+          tc_cp_sf(sfb, sdesc_sf(smem_u32(bsf + st * C::SF_BYTES + kk * SF_BLOCK)));
+          const uint32_t a0 = smem_u32(abuf + st * C::A_BYTES + kk * A_TILE);
+          const uint32_t b0 = smem_u32(bbuf + st * C::B_BYTES + kk * C::B_TILE);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_mxf8f6f4(d, sdesc_sw128(a0 + ks * 32), sdesc_sw128(b0 + ks * 32), idesc_with_sf(IDESC, ks, ks), sfa, sfb,
+                         !(first && kk == 0 && ks == 0));
+        }
+        tc_commit(&S.empty[st]);
+        if (last) tc_commit(&S.accf[b]);
+      }
+      __syncwarp();
+      slot = (slot + UK) % SF_SLOTS;
+      first = last;
+      if (last) ++seg;
+      if (++st == C::STAGES) { st = 0; ph ^= 1; }
+      if (++ku == KU) ku = 0;
+    }
+    if (!ok) drain();
+    __syncwarp();
+  } else if (warp < WARP_EPI0) {
+    if constexpr (!C::PRE) {
+    // ------------------------------------------------ token operand
+    // A lane owns 8 of the unit's 256 K; warp wi of the unit's gw takes tokens wi, wi + gw, ...
+    const int sw = warp - WARP_SPLIT0, grp = sw / gw, ngrp = SPLIT_WARPS / gw, wi = sw % gw;
+    const int kk = lane >> 4, g8 = lane & 15;
+    constexpr int IP = MT / 8;                  // tokens per warp at most
+    int64_t tile = u0 / KU;
+    int ku = static_cast<int>(u0 - tile * KU), tt = static_cast<int>(tile % TT);
+    const int nu = static_cast<int>(u1 - u0);
+    auto advance = [&](int n) {
+      ku += n;
+      while (ku >= KU) { ku -= KU; if (++tt == TT) tt = 0; }
+    };
+    auto load = [&](uint4 (&v)[IP]) {
+      const int k = ku * (UK * 128) + lane * 8;
+#pragma unroll
+      for (int i = 0; i < IP; ++i) {
+        const int tl = i * gw + wi, t = tt * MT + tl;
+        v[i] = (tl < MT && t < p.M && k < p.K) ? __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.ldx + k))
+                                               : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    // PD units' loads in flight: a unit is consumed faster than L2 answers
+    constexpr int PD = IP <= 2 ? 4 : IP <= 4 ? 2 : 1;
+    constexpr int JB = IP < 4 ? IP : 4;
+    uint4 buf[PD][IP];
+    advance(grp);
+    int ahead = grp;   // unit whose loads go out next
+#pragma unroll
+    for (int d = 0; d < PD; ++d) {
+      if (ahead < nu) load(buf[d]);
+      advance(ngrp);
+      ahead += ngrp;
+    }
+    bool ok = true;
+    for (int i0 = grp; i0 < nu && ok; i0 += PD * ngrp) {
+#pragma unroll
+      for (int d = 0; d < PD; ++d) {
+        const int i = i0 + d * ngrp;
+        if (i >= nu) break;
+        const int st = i % C::STAGES;
+        if (!mbar_wait(&S.empty[st], ((i / C::STAGES) & 1) ^ 1, deadline, abort_flag)) { fail(5); ok = false; break; }
+        __syncwarp();
+        uint8_t* tb = bbuf + st * C::B_BYTES + kk * C::B_TILE;
+        uint8_t* sf = bsf + st * C::SF_BYTES + kk * SF_BLOCK;
+#pragma unroll
+        for (int j = 0; j < IP; j += JB)
+          if (j * gw + wi < mtile) split_items<JB>(buf[d] + j, tb, sf, j * gw + wi, gw, MT, g8);   // warp-uniform
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.full[st]);
+        if (ahead < nu) load(buf[d]);
+        advance(ngrp);
+        ahead += ngrp;
+      }
+    }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ sums
+    const int q = warp & 3, row = 32 * q + lane;   // TMEM lane quarter = warp % 4
+    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    constexpr int TB = MT < 16 ? MT : 16;   // tokens per TMEM read
+    constexpr int CB = 64 / TB;             // parts per batch: 64 loads in flight
+    int seg = 0;
+    bool ok = true;
+    for (int64_t u = u0; u < u1 && ok; ++seg) {
+      const int64_t tile = u / KU, t0 = tile * KU, t1 = t0 + KU, ue = min(t1, u1);
+      const int rt = static_cast<int>(tile / TT), tt = static_cast<int>(tile - (int64_t)rt * TT);
+      const int m = min(MT, p.M - tt * MT), n = rt * 128 + row;
+      const bool mine = u == t0;                           // this share starts the tile and so finishes it
+      const int c1 = mine ? share_of(U, G, t1 - 1) : share;   // shares after this one that hold parts of it
+      const int b = seg & 1;
+      const float bv = (p.bias && n < p.N) ? __ldg(p.bias + n) : 0.0f;
+      if (!mbar_wait(&S.accf[b], (seg >> 1) & 1, deadline, abort_flag)) { fail(7); break; }
+      __syncwarp();
+      tc_fence_after();
+#pragma unroll 1
+      for (int tb = 0; tb < m && ok; tb += TB) {
+        float v[TB];
+        if constexpr (NC == 16) {
+          float a[16];
+          tmem_ld16(tl + b * NC, a);
+          tmem_ld_wait();
+#pragma unroll
+          for (int t = 0; t < TB; ++t) v[t] = a[t] + a[MT + t];
+        } else {
+          float a[16], c[16];
+          tmem_ld16(tl + b * NC + tb, a);
+          tmem_ld16(tl + b * NC + MT + tb, c);
+          tmem_ld_wait();
+#pragma unroll
+          for (int t = 0; t < TB; ++t) v[t] = a[t] + c[t];
+        }
+        if (!mine) {
+          uint32_t* dst = p.part + ((int64_t)share * MT + tb) * 128 + row;
+#pragma unroll
+          for (int t = 0; t < TB; ++t)
+            if (tb + t < m && !(p.test_withhold && share == G - 1)) part_put(dst + t * 128, v[t]);
+          continue;
+        }
+#pragma unroll 1
+        for (int cb = share + 1; cb <= c1 && ok; cb += CB) {   // the later shares' parts, in K order
+          uint32_t w[CB][TB];
+          uint32_t spins = 0;
+          for (;;) {
+            bool all = true;
+#pragma unroll
+            for (int i = 0; i < CB; ++i) {
+              const uint32_t* src = p.part + ((int64_t)min(cb + i, c1) * MT + tb) * 128 + row;
+#pragma unroll
+              for (int t = 0; t < TB; ++t) w[i][t] = tb + t < m ? part_peek(src + t * 128) : 1u;
+            }
+#pragma unroll
+            for (int i = 0; i < CB; ++i)
+#pragma unroll
+              for (int t = 0; t < TB; ++t) all &= w[i][t] != 0u;
+            if (all) break;
+            if ((++spins & 15u) == 0 && (*abort_flag || globaltimer() > deadline)) { fail(8); ok = false; break; }
+          }
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < CB; ++i) {
+            if (cb + i > c1) break;
+            uint32_t* src = p.part + ((int64_t)(cb + i) * MT + tb) * 128 + row;
+#pragma unroll
+            for (int t = 0; t < TB; ++t) {
+              v[t] += part_value(w[i][t]);
+              if (tb + t < m) __stcg(src + t * 128, 0u);   // empty again for the next call
+            }
+          }
+        }
+        if (n < p.N && ok) {
+#pragma unroll
+          for (int t = 0; t < TB; ++t) {
+            if (tb + t >= m) break;
+            const int64_t o = (int64_t)(tt * MT + tb + t) * p.ldo + n;
+            if (p.out_f32) reinterpret_cast<float*>(p.out)[o] = v[t] + bv;
+            else reinterpret_cast<uint16_t*>(p.out)[o] = bf16_bits(v[t] + bv);
+          }
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.acce[b]);
+      u = ue;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == WARP_EPI0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Row-major MXFP4 [N][K/2] + [N][K/32] -> tiles: [N/128][K/128] blocks of 128
+// rows x 64 code bytes, then as many 512-byte scale blocks, the rest padded
+// with zero codes and unit scales.
+__global__ void __launch_bounds__(256) k_pack_w4(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s, int N, int K,
+                                                 int KC, uint8_t* __restrict__ codes, uint8_t* __restrict__ sf) {
+  const int64_t blk = blockIdx.x;
+  const int rt = static_cast<int>(blk / KC), kc = static_cast<int>(blk % KC);
+  for (int i = threadIdx.x; i < 512; i += 256) {   // 512 groups of 32: 16 bytes of codes, one scale
+    const int r = i >> 2, g = i & 3, n = rt * 128 + r, k = kc * 128 + g * 32;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    uint8_t sc = 127;
+    if (n < N && k < K) {
+      v = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)n * (K / 2) + k / 2));
+      sc = __ldg(s + (int64_t)n * (K / 32) + k / 32);
+    }
+    reinterpret_cast<uint4*>(codes + blk * w4::CODE_BLOCK)[i] = v;
+    sf[blk * w4::SF_BLOCK + w4::sf_byte(r, g)] = sc;
+  }
+}
+
+// The tokens' operand columns and scales, [token tile][K/128] blocks of NC x
+// 128 bytes (the tile as the MMA reads it) and of 512 bytes: 16 lanes a chunk of
+// one token, 16 tokens a CTA.
+template <int NC>
+__global__ void __launch_bounds__(256) k_split_x(const LinearParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int MT = NC / 2;
+  const int kc = blockIdx.x, t = blockIdx.y * 16 + (threadIdx.x >> 4), g8 = threadIdx.x & 15, k = kc * 128 + g8 * 8;
+  const uint4 v = (t < p.M && k < p.K) ? __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.ldx + k))
+                                       : make_uint4(0u, 0u, 0u, 0u);
+  const int64_t blk = (int64_t)(t / MT) * p.KC + kc;
+  if (t / MT < p.TT) split_items<1>(&v, p.xop + blk * (NC * 128), p.xsf + blk * SF_BLOCK, t % MT, 0, MT, g8);
+}
+
+template <int NC>
+static cudaError_t launch(const CUtensorMap& w, const LinearParams& p, int grid, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};   // devices on which the kernel may take its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
+    e = cudaFuncSetAttribute(k_linear_w4<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NC>());
+    if (e != cudaSuccess) return e;
+    if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
+  // The kernel's set-up may overlap the tail of the call before it.
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(Cfg<NC>::THREADS);
+  cfg.dynamicSmemBytes = smem_bytes<NC>();
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if constexpr (Cfg<NC>::PRE) {
+    cudaLaunchConfig_t pre = cfg;
+    pre.gridDim = dim3(p.KC, (p.M + 15) / 16);
+    pre.blockDim = dim3(256);
+    pre.dynamicSmemBytes = 0;
+    if ((e = cudaLaunchKernelEx(&pre, k_split_x<NC>, p)) != cudaSuccess) return e;
+  }
+  return cudaLaunchKernelEx(&cfg, k_linear_w4<NC>, w, p);
+}
+
+}  // namespace linear
+
+cudaError_t launch_linear_w4(const CUtensorMap& w, const LinearParams& p, int nc, int grid, cudaStream_t st) {
+  switch (nc) {
+    case 16: return linear::launch<16>(w, p, grid, st);
+    case 32: return linear::launch<32>(w, p, grid, st);
+    case 64: return linear::launch<64>(w, p, grid, st);
+    default: return linear::launch<128>(w, p, grid, st);
+  }
+}
+
+cudaError_t launch_pack_w4(const uint8_t* q, const uint8_t* s, int N, int K, uint8_t* packed, cudaStream_t st) {
+  const int RT = (N + 127) / 128, KC = (K + 127) / 128;
+  const int64_t blocks = (int64_t)RT * KC;
+  linear::k_pack_w4<<<(unsigned)blocks, 256, 0, st>>>(q, s, N, K, KC, packed, packed + blocks * w4::CODE_BLOCK);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

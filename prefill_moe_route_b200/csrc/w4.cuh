@@ -1,0 +1,105 @@
+// w4.cuh -- device helpers of the few-token operators (linear.cu, layer.cu):
+// MXFP4 weights against bf16 activations on the tensor cores, without rounding
+// the activations.
+//
+// kind::mxf8f6f4 multiplies E2M1 weights (scale per 32 along K) by E4M3
+// operands (scale per 32 along K) into fp32.  A bf16 activation has an 8-bit
+// significand and an E4M3 value a 4-bit one, so an activation block of 32 is
+// written as two operand columns that share the weights:
+//   hi = E4M3(v / 2^s),            s = floor(log2 amax) - 7
+//   lo = E4M3((v / 2^s - hi) * 32) with scale 2^(s - 5)
+// |v| / 2^s < 256, so hi never saturates; the rest is at most 8 and has at most
+// 4 significant bits, so hi + lo / 32 is v / 2^s exactly while |v| >= 2^-14
+// amax; smaller values of the block keep an absolute error of 2^-21 amax.  An
+// fp32 value (not bf16) is kept to 2^-9 relative, half of bf16's rounding.
+// Subnormal bf16 activations (below 2^-126) count as zero.
+// A block that holds an infinity or a NaN becomes NaN in both columns, so only
+// its own token's sums become NaN.
+#pragma once
+#include "internal.h"
+#include "ptx.cuh"
+#include "codec.cuh"
+
+namespace moe {
+namespace w4 {
+
+constexpr int A_TILE = 16384;      // 128 rows x 128 E2M1 in shared memory (8 bytes of codes in each 16)
+constexpr int SF_BLOCK = 512;      // scales of 128 rows x 4 groups, in the tensor cores' order
+constexpr int CODE_BLOCK = 8192;   // the same tile's codes in global memory
+
+// Scale exponent of a block from its largest magnitude; SPLIT_NAN marks a
+// block that is not finite.
+constexpr int SPLIT_NAN = -128;
+__device__ __forceinline__ int split_exp(float amax) {
+  const int ex = static_cast<int>(__float_as_uint(amax) >> 23);   // amax >= 0
+  if (ex == 255) return SPLIT_NAN;
+  return max(-112, ex - 134);   // floor(log2 amax) - 7, in the range of lo's scale and of f16x2_scaled
+}
+__device__ __forceinline__ uint32_t split_code_hi(int s) { return s == SPLIT_NAN ? 127u : static_cast<uint32_t>(s + 127); }
+__device__ __forceinline__ uint32_t split_code_lo(int s) { return s == SPLIT_NAN ? 127u : static_cast<uint32_t>(s + 122); }
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Two bf16 divided by 2^s as f16, by integer arithmetic on the fields (the
+// conversion unit is the scarce one here): magnitudes below 2^-14 after the
+// scaling become zero, 2^-21 of the block's largest.
+__device__ __forceinline__ uint32_t f16x2_scaled(uint32_t w, int s) {
+  const uint32_t off = static_cast<uint32_t>(s + 112) * 0x00800080u;   // exponent fields: e - 127 - s + 15 = e - (s + 112)
+  const uint32_t m = max_u16x2(w & 0x7FFF7FFFu, off) - off;
+  return (m << 3) | (w & 0x80008000u);
+}
+
+// hi and lo codes of two values already divided by 2^s, as f16.
+__device__ __forceinline__ void split_f16x2(uint32_t v, uint32_t& hi, uint32_t& lo) {
+  uint16_t h, l;
+  uint32_t back, r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(v));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(back));        // exact
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x50005000u));   // times 32
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(r));
+  hi = h;
+  lo = l;
+}
+
+// Two fp32 values divided by 2^s (inv = 2^-s) as f16.
+__device__ __forceinline__ uint32_t f16x2_of(float a, float b, float inv) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b * inv), "f"(a * inv));
+  return r;
+}
+
+// Byte of value k (0..127) of operand row n in a 128-byte-swizzled tile.
+__device__ __forceinline__ uint32_t tile_byte(uint32_t n, uint32_t k) {
+  return n * 128u + ((((k >> 4) ^ (n & 7u)) << 4) | (k & 15u));
+}
+// Byte of row n's scale of group q (0..3) in a 512-byte scale block.
+__device__ __forceinline__ uint32_t sf_byte(uint32_t n, uint32_t q) { return 16u * (n & 31u) + 4u * (n >> 5) + q; }
+
+// A part of a sum on its way to another CTA: the word is the value's bits
+// inverted, so that zero (what the buffer holds between calls) marks a part
+// that has not arrived.  Value and arrival are one 4-byte word: no fence, no
+// flag, one trip through L2.  The reader puts the zero back.
+__device__ __forceinline__ void part_put(uint32_t* p, float v) {
+  const uint32_t bits = v == v ? __float_as_uint(v) : 0x7FC00000u;   // any NaN as the one whose inverse is not zero
+  asm volatile("st.relaxed.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(~bits) : "memory");
+}
+__device__ __forceinline__ uint32_t part_peek(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float part_value(uint32_t word) { return __uint_as_float(~word); }
+
+// Units [lo, hi) of `total` that share c of `g` shares takes, and the share that holds unit u.
+__device__ __forceinline__ int64_t share_begin(int64_t total, int g, int c) { return total * c / g; }
+__device__ __forceinline__ int share_of(int64_t total, int g, int64_t u) {
+  return static_cast<int>(((u + 1) * g - 1) / total);
+}
+
+}  // namespace w4
+}  // namespace moe
