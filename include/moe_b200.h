@@ -374,6 +374,49 @@ MOE_API int moe_linear_w4_workspace_size(const moe_linear_shape_t* shape, size_t
 MOE_API int moe_linear_w4(const moe_linear_shape_t* shape, const void* x, const void* w_packed, const float* bias,
                           void* out, void* workspace, size_t ws_bytes, void* stream);
 
+/* A whole mixture-of-experts layer for a few tokens (M <= 16), in two launches:
+ *   h      = x * rsqrt(mean(x^2) + norm_eps) * norm_w   (norm_w NULL: h = x)
+ *   logits = h . router_w^T, s = sigmoid(logits), top-k of s + bias (ties ->
+ *            lower expert ID), w_j = s_j / sum_j s_j * routed_scale (as moe_route)
+ *   y      = sum_j w_j * E_j(h) + E_shared(h),
+ *            E(h) = (silu(h . gate^T) * (h . up^T)) . down^T
+ *   out    = bf16( y (+ x with add_residual) )
+ * h is not rounded for the router (fp32 products); for the experts h and the
+ * SwiGLU output are held to 2^-9 of each value (h is exact without a norm).
+ * H, I, shared_I multiples of 128 (shared_I 0: no shared expert), E <= 512,
+ * topk <= min(E, 16); ldx, ldo: elements between rows (>= H, ldx % 8 == 0).  */
+typedef struct {
+  int32_t M, H, I, E, topk, shared_I, add_residual;
+  float routed_scale, norm_eps;
+  int64_t ldx, ldo;
+} moe_layer_shape_t;
+
+/* Device pointers of a layer's weights: the layouts of moe_forward, so one
+ * copy of an expert's weights serves both.
+ *   norm_w   bf16 [H] or NULL;  router_w bf16 [E][H];  bias fp32 [E] or NULL
+ *   w13, w13_scales, w2, w2_scales   as moe_forward's MXFP4 arguments
+ *   shared_* the same of one expert of width shared_I (ignored when 0)       */
+typedef struct {
+  const void *norm_w, *router_w;
+  const float* bias;
+  const void *w13, *w13_scales, *w2, *w2_scales;
+  const void *shared_w13, *shared_w13_scales, *shared_w2, *shared_w2_scales;
+} moe_layer_weights_t;
+
+/* Workspace bytes of moe_layer_w4 (host only, pure; the same for every M).   */
+MOE_API int moe_layer_w4_workspace_size(const moe_layer_shape_t* shape, size_t* bytes);
+
+/* The layer.  x bf16, 16-byte aligned; out bf16 (must not overlap an input);
+ * topk_ids int32 [M][topk] and topk_w fp32 [M][topk] out, or NULL.  Weights
+ * 32-byte, scales, norm_w and router_w 16-byte aligned.  A token whose row
+ * holds an infinity or a NaN gives NaN (its expert choice is then unspecified,
+ * within range).  The workspace is zero-filled once (moe_workspace_init) and
+ * then serves any sequence of moe_layer_w4 calls on one stream, of any shapes
+ * it is large enough for; moe_get_status reports a device-side wait that ran
+ * out (zero-fill the workspace then).  MOE_TEST_WITHHOLD_FLAG applies.       */
+MOE_API int moe_layer_w4(const moe_layer_shape_t* shape, const moe_layer_weights_t* weights, const void* x, void* out,
+                         int32_t* topk_ids, float* topk_w, void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

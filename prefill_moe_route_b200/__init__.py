@@ -21,6 +21,7 @@ __all__ = [
     "moe_forward", "moe_forward_routed", "moe_forward_partial", "moe_round_bf16", "moe_forward_timed", "moe_forward_static", "moe_get_status_static", "moe_launches_per_call", "MOE_STATIC_SCRATCH_BYTES", "moe_get_status", "moe_quantize_mxfp4", "moe_pack_mxfp4_scales", "moe_quantize_fp8_block128",
     "MOE_OUT_BF16", "MOE_OUT_F32", "MoeLinearShape", "moe_w4_packed_size", "moe_pack_w4",
     "moe_linear_w4_workspace_size", "moe_linear_w4",
+    "MoeLayerShape", "MoeLayerWeights", "moe_layer_w4_workspace_size", "moe_layer_w4",
     "moe_probe_tensor_peak", "MOE_PROBE_FP8", "MOE_PROBE_FP4", "MOE_PROBE_BF16",
 ]
 
@@ -74,6 +75,36 @@ class MoeLinearShape(ctypes.Structure):
         return cls(M, N, K, out_type, K if ldx is None else ldx, N if ldo is None else ldo)
 
 
+class MoeLayerShape(ctypes.Structure):
+    """Shape of moe_layer_w4; a program that repeats a call keeps one."""
+    _fields_ = [("M", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("topk", ctypes.c_int32), ("shared_I", ctypes.c_int32), ("add_residual", ctypes.c_int32),
+                ("routed_scale", ctypes.c_float), ("norm_eps", ctypes.c_float),
+                ("ldx", ctypes.c_int64), ("ldo", ctypes.c_int64)]
+
+    @classmethod
+    def of(cls, M, H, I, E, topk, routed_scale, shared_I=0, norm_eps=1e-5, add_residual=False, ldx=None, ldo=None):
+        return cls(M, H, I, E, topk, shared_I, int(add_residual), routed_scale, norm_eps,
+                   H if ldx is None else ldx, H if ldo is None else ldo)
+
+
+class MoeLayerWeights(ctypes.Structure):
+    """Device pointers of moe_layer_w4's weights; `of` keeps the tensors alive."""
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("norm_w", "router_w", "bias", "w13", "w13_scales", "w2", "w2_scales",
+                 "shared_w13", "shared_w13_scales", "shared_w2", "shared_w2_scales")]
+
+    @classmethod
+    def of(cls, *, router_w, w13, w13_scales, w2, w2_scales, norm_w=None, bias=None, shared_w13=None,
+           shared_w13_scales=None, shared_w2=None, shared_w2_scales=None):
+        held = dict(norm_w=norm_w, router_w=router_w, bias=bias, w13=w13, w13_scales=w13_scales, w2=w2,
+                    w2_scales=w2_scales, shared_w13=shared_w13, shared_w13_scales=shared_w13_scales,
+                    shared_w2=shared_w2, shared_w2_scales=shared_w2_scales)
+        w = cls(**{n: _ptr(t) for n, t in held.items()})
+        w.tensors = held
+        return w
+
+
 class _Layout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint64) for n in
                 ("status", "topk_ids", "topk_w", "counts", "offsets", "sorted_pairs", "inv",
@@ -115,6 +146,8 @@ def load():
         "moe_pack_w4": [P, P, I32, I32, P, P],
         "moe_linear_w4_workspace_size": [ctypes.POINTER(MoeLinearShape), ctypes.POINTER(SZ)],
         "moe_linear_w4": [ctypes.POINTER(MoeLinearShape), P, P, P, P, P, SZ, P],
+        "moe_layer_w4_workspace_size": [ctypes.POINTER(MoeLayerShape), ctypes.POINTER(SZ)],
+        "moe_layer_w4": [ctypes.POINTER(MoeLayerShape), ctypes.POINTER(MoeLayerWeights), P, P, P, P, P, SZ, P],
         "moe_probe_tensor_peak": [I32, I32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double), P],
     }
     for name, args in sig.items():
@@ -312,3 +345,17 @@ def moe_linear_w4(shape: MoeLinearShape, x, w_packed, bias, out, workspace, ws_b
     rc = load().moe_linear_w4(ctypes.byref(shape), _ptr(x), _ptr(w_packed), _ptr(bias), _ptr(out), _ptr(workspace),
                               ws_bytes, _stream(stream))
     return _ret(rc, "moe_linear_w4", check)
+
+
+def moe_layer_w4_workspace_size(shape: MoeLayerShape) -> int:
+    n = ctypes.c_size_t(0)
+    _ret(load().moe_layer_w4_workspace_size(ctypes.byref(shape), ctypes.byref(n)), "moe_layer_w4_workspace_size", True)
+    return n.value
+
+
+def moe_layer_w4(shape: MoeLayerShape, weights: MoeLayerWeights, x, out, topk_ids, topk_w, workspace, ws_bytes: int,
+                 stream=None, check: bool = True) -> int:
+    """A whole MoE layer for a few tokens: norm, router, top-k, experts, shared expert, residual."""
+    rc = load().moe_layer_w4(ctypes.byref(shape), ctypes.byref(weights), _ptr(x), _ptr(out), _ptr(topk_ids),
+                             _ptr(topk_w), _ptr(workspace), ws_bytes, _stream(stream))
+    return _ret(rc, "moe_layer_w4", check)

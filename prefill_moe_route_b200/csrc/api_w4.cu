@@ -3,6 +3,7 @@
 // maps and launches.  Nothing here synchronizes the host.
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstring>
 
 #include "host.h"
@@ -11,6 +12,8 @@ namespace moe {
 
 cudaError_t launch_linear_w4(const CUtensorMap& w, const LinearParams& p, int nc, int grid, cudaStream_t st);
 cudaError_t launch_pack_w4(const uint8_t* q, const uint8_t* s, int N, int K, uint8_t* packed, cudaStream_t st);
+
+cudaError_t launch_layer_w4(const CUtensorMap* maps, const LayerParams& p, int sms, cudaStream_t st);
 
 constexpr int kMaxGrid = 148;              // CTAs of these kernels: one per SM of a B200
 constexpr size_t kLinearHeader = 256;      // status words
@@ -45,6 +48,42 @@ static int linear_plan(const moe_linear_shape_t& s, int sms, LinearPlan* p) {
     p->total = p->o_xsf + (size_t)p->TT * p->KC * 512;
   }
   return MOE_OK;
+}
+
+struct LayerPlan {
+  size_t o_part1, o_part2, o_rstd, o_sig, o_key, o_xop, o_xsf, o_mop, o_msf, total;
+};
+
+static int layer_plan(const moe_layer_shape_t& s, LayerPlan* p) {
+  if (s.M < 1 || s.E < 1 || s.topk < 1 || s.H < 128 || s.I < 128 || s.shared_I < 0) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(s.routed_scale) || !(s.norm_eps >= 0.0f) || !std::isfinite(s.norm_eps)) return MOE_ERR_INVALID_ARG;
+  if (s.ldx < s.H || s.ldo < s.H || s.ldx % 8) return MOE_ERR_INVALID_ARG;
+  if (s.M > 16 || s.E > kMaxE || s.topk > kMaxTopk || s.topk > s.E) return MOE_ERR_UNSUPPORTED;
+  if (s.H % 128 || s.I % 128 || s.shared_I % 128 || s.H > 65536 || s.I > 65536 || s.shared_I > 65536)
+    return MOE_ERR_UNSUPPORTED;
+  // One layout for every M.  The parts come first, in one place for every
+  // shape: they are zero between calls, the rest is written before it is read.
+  size_t o = 256;
+  auto take = [&](size_t bytes) { size_t r = o; o = align_up(o + bytes, 256); return r; };
+  const size_t KC = s.H / 128, tiles = (size_t)std::min(s.E, 16 * s.topk) * (s.I / 128) + s.shared_I / 128;
+  p->o_part1 = take((size_t)kMaxGrid * 32 * 128 * 4);
+  p->o_part2 = take((size_t)kMaxGrid * 16 * 128 * 4);
+  p->o_rstd = take(16 * 4);
+  p->o_sig = take((size_t)16 * s.E * 4);
+  p->o_key = take((size_t)16 * s.E * 4);
+  p->o_xop = take(KC * 32 * 128);
+  p->o_xsf = take(KC * 512);
+  p->o_mop = take(tiles * 32 * 128);
+  p->o_msf = take(tiles * 512);
+  p->total = o;
+  return MOE_OK;
+}
+
+// Tensor map of `batch` 4-bit matrices [rows][K], boxes of 128 x 128 (tiles land unpacked).
+static bool mx_map(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_t batch) {
+  const uint64_t d[3] = {K, rows, batch}, st[2] = {K / 2, rows * (K / 2)};
+  const uint32_t box[3] = {128, 128, 1};
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, base, d, st, box);
 }
 
 }  // namespace moe
@@ -120,6 +159,79 @@ int moe_linear_w4(const moe_linear_shape_t* shape, const void* x, const void* w_
   p.timeout_ns = wait_timeout_ns();
   const cudaError_t e = launch_linear_w4(map, p, pl.nc, pl.grid, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "moe_linear_w4 kernel launch", e);
+}
+
+int moe_layer_w4_workspace_size(const moe_layer_shape_t* shape, size_t* bytes) {
+  if (!shape || !bytes) return fail(MOE_ERR_INVALID_ARG, "moe_layer_w4_workspace_size: null pointer argument");
+  LayerPlan p;
+  const int rc = layer_plan(*shape, &p);
+  if (rc != MOE_OK) return fail(rc, "moe_layer_w4: unsupported shape");
+  *bytes = p.total;
+  return MOE_OK;
+}
+
+int moe_layer_w4(const moe_layer_shape_t* shape, const moe_layer_weights_t* w, const void* x, void* out, int32_t* topk_ids,
+                 float* topk_w, void* workspace, size_t ws_bytes, void* stream) {
+  if (!shape || !w || !x || !out || !workspace || !w->router_w || !w->w13 || !w->w13_scales || !w->w2 || !w->w2_scales)
+    return fail(MOE_ERR_INVALID_ARG, "moe_layer_w4: null pointer argument");
+  LayerPlan pl;
+  const int rc = layer_plan(*shape, &pl);
+  if (rc != MOE_OK) return fail(rc, "moe_layer_w4: unsupported shape");
+  const bool shared = shape->shared_I > 0;
+  if (shared && (!w->shared_w13 || !w->shared_w13_scales || !w->shared_w2 || !w->shared_w2_scales))
+    return fail(MOE_ERR_INVALID_ARG, "moe_layer_w4: null shared expert pointer with shared_I > 0");
+  const void* sh[4] = {shared ? w->shared_w13 : nullptr, shared ? w->shared_w13_scales : nullptr,
+                       shared ? w->shared_w2 : nullptr, shared ? w->shared_w2_scales : nullptr};
+  const void* ptrs[16] = {x, out, workspace, topk_ids, topk_w, w->norm_w, w->router_w, w->bias, w->w13, w->w13_scales,
+                          w->w2, w->w2_scales, sh[0], sh[1], sh[2], sh[3]};
+  for (int i : {0, 5, 6, 9, 11, 13, 15})
+    if (!aligned(ptrs[i], 16)) return fail(MOE_ERR_INVALID_ARG, "moe_layer_w4: pointer not 16-byte aligned");
+  for (int i : {8, 10, 12, 14})
+    if (!aligned(ptrs[i], 32)) return fail(MOE_ERR_INVALID_ARG, "moe_layer_w4: weights need 32-byte alignment");
+  if (!aligned(workspace, 256) || !aligned(out, 2) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) || !aligned(w->bias, 4))
+    return fail(MOE_ERR_INVALID_ARG, "moe_layer_w4: workspace needs 256-byte alignment, out, ids, weights and bias their type's");
+  if (out == x || out == workspace) return fail(MOE_ERR_INVALID_ARG, "moe_layer_w4: out aliases an input");
+  const int dev = resolve_device(stream, ptrs, 16);
+  if (dev < 0) return dev;
+  DeviceGuard g(dev);
+  if (ws_bytes < pl.total) return fail(MOE_ERR_WORKSPACE, "moe_layer_w4: workspace smaller than moe_layer_w4_workspace_size");
+  const uint64_t H = shape->H, I = shape->I, E = shape->E, S = shape->shared_I;
+  CUtensorMap m[4];
+  bool ok = mx_map(&m[0], w->w13, H, 2 * I, E) && mx_map(&m[1], w->w2, I, H, E);
+  if (shared) ok = ok && mx_map(&m[2], sh[0], H, 2 * S, 1) && mx_map(&m[3], sh[2], S, H, 1);
+  else { m[2] = m[0]; m[3] = m[1]; }
+  if (!ok) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor map");
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  LayerParams p = {};
+  p.x = static_cast<const uint16_t*>(x);
+  p.norm_w = static_cast<const uint16_t*>(w->norm_w);
+  p.router_w = static_cast<const uint16_t*>(w->router_w);
+  p.bias = w->bias;
+  p.s13 = static_cast<const uint8_t*>(w->w13_scales);
+  p.s2 = static_cast<const uint8_t*>(w->w2_scales);
+  p.ss13 = static_cast<const uint8_t*>(sh[1]);
+  p.ss2 = static_cast<const uint8_t*>(sh[3]);
+  p.out = static_cast<uint16_t*>(out);
+  p.ids_out = topk_ids;
+  p.wts_out = topk_w;
+  p.status = reinterpret_cast<int32_t*>(ws);
+  p.sync = reinterpret_cast<int32_t*>(ws + 64);
+  p.part1 = reinterpret_cast<uint32_t*>(ws + pl.o_part1);
+  p.part2 = reinterpret_cast<uint32_t*>(ws + pl.o_part2);
+  p.rstd = reinterpret_cast<float*>(ws + pl.o_rstd);
+  p.sig = reinterpret_cast<float*>(ws + pl.o_sig);
+  p.key = reinterpret_cast<uint32_t*>(ws + pl.o_key);
+  p.xop = ws + pl.o_xop; p.xsf = ws + pl.o_xsf;
+  p.mop = ws + pl.o_mop; p.msf = ws + pl.o_msf;
+  p.ldx = shape->ldx; p.ldo = shape->ldo;
+  p.M = shape->M; p.H = shape->H; p.I = shape->I; p.S = shape->shared_I; p.E = shape->E; p.topk = shape->topk;
+  p.nc = shape->M <= 8 ? 16 : 32;
+  p.residual = shape->add_residual != 0;
+  p.scale = shape->routed_scale; p.eps = shape->norm_eps;
+  p.test_withhold = take_withhold();
+  p.timeout_ns = wait_timeout_ns();
+  const cudaError_t e = launch_layer_w4(m, p, std::min(sm_count(dev), kMaxGrid), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "moe_layer_w4 kernel launch", e);
 }
 
 }  // extern "C"

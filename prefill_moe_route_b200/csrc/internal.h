@@ -160,4 +160,29 @@ struct LinearParams {
   uint64_t timeout_ns;
 };
 
+// Parameters of the few-token MoE layer (layer.cu).
+struct LayerParams {
+  const uint16_t* x;        // bf16, rows ldx elements apart
+  const uint16_t* norm_w;   // bf16 [H], or null: no norm
+  const uint16_t* router_w; // bf16 [E][H]
+  const float* bias;        // fp32 [E], or null
+  const uint8_t *s13, *s2, *ss13, *ss2;   // packed weight scales: routed, shared
+  uint16_t* out;            // bf16, rows ldo elements apart
+  int32_t* ids_out;         // [M][topk], or null
+  float* wts_out;           // [M][topk], or null
+  int32_t* status;
+  int32_t* sync;            // [0] next task, [1] quarters of mid tiles stored; k_layer_head zeroes both
+  uint32_t *part1, *part2;  // parts of cut tiles: [grid][gate, up of the tokens][128], [grid][tokens][128]; zero between calls
+  float *rstd, *sig;        // [M], [M][E]
+  uint32_t* key;            // [M][E] selection keys
+  uint8_t *xop, *xsf;       // the tokens' operand blocks and scale blocks [H/128]
+  uint8_t *mop, *msf;       // mid's, one per GEMM1 tile
+  int64_t ldx, ldo;
+  int M, H, I, S, E, topk;  // S: the shared expert's width, 0 without one
+  int nc;                   // operand columns: 16 up to 8 tokens, else 32
+  int residual, test_withhold;
+  float scale, eps;
+  uint64_t timeout_ns;
+};
+
 }  // namespace moe

@@ -63,3 +63,45 @@ def test_linear_refuses_pointers_before_any_launch():
 def test_workspace_parts_come_first_and_grow_with_the_token_tile():
     sizes = [moe.moe_linear_w4_workspace_size(_linear(M=m)) for m in (1, 8, 9, 16, 17, 32, 33, 64, 65)]
     assert sizes == sorted(sizes) and sizes[0] == sizes[1] and sizes[2] == sizes[3]
+
+
+def _layer(**kw):
+    d = dict(M=4, H=512, I=256, E=8, topk=2, shared_I=128, add_residual=1, routed_scale=1.0, norm_eps=1e-5, ldx=512, ldo=512)
+    d.update(kw)
+    return moe.MoeLayerShape(**d)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(M=0), moe.MOE_ERR_INVALID_ARG), (dict(E=0), moe.MOE_ERR_INVALID_ARG), (dict(topk=0), moe.MOE_ERR_INVALID_ARG),
+    (dict(shared_I=-128), moe.MOE_ERR_INVALID_ARG), (dict(ldx=504), moe.MOE_ERR_INVALID_ARG),
+    (dict(ldx=516), moe.MOE_ERR_INVALID_ARG), (dict(ldo=511), moe.MOE_ERR_INVALID_ARG),
+    (dict(routed_scale=float("inf")), moe.MOE_ERR_INVALID_ARG), (dict(norm_eps=float("nan")), moe.MOE_ERR_INVALID_ARG),
+    (dict(norm_eps=-1.0), moe.MOE_ERR_INVALID_ARG), (dict(M=17), moe.MOE_ERR_UNSUPPORTED),
+    (dict(E=513), moe.MOE_ERR_UNSUPPORTED), (dict(topk=9), moe.MOE_ERR_UNSUPPORTED),
+    (dict(E=64, topk=17), moe.MOE_ERR_UNSUPPORTED), (dict(H=576, ldx=576, ldo=576), moe.MOE_ERR_UNSUPPORTED),
+    (dict(I=192), moe.MOE_ERR_UNSUPPORTED), (dict(shared_I=64), moe.MOE_ERR_UNSUPPORTED)])
+def test_layer_refuses_shapes(bad, code):
+    n = ctypes.c_size_t(0)
+    assert moe.load().moe_layer_w4_workspace_size(ctypes.byref(_layer(**bad)), ctypes.byref(n)) == code
+
+
+def test_layer_workspace_does_not_depend_on_the_token_count():
+    assert len({moe.moe_layer_w4_workspace_size(_layer(M=m)) for m in (1, 8, 9, 16)}) == 1
+
+
+def test_layer_refuses_pointers_before_any_launch():
+    names = ["norm_w", "router_w", "bias", "w13", "w13_scales", "w2", "w2_scales", "shared_w13", "shared_w13_scales",
+             "shared_w2", "shared_w2_scales"]
+    good = {n: 4096 * (i + 1) for i, n in enumerate(names)}
+
+    def call(shape=None, x=1 << 20, out=1 << 21, ws=1 << 22, ids=None, wts=None, **kw):
+        w = moe.MoeLayerWeights.of(**dict(good, **kw))
+        return moe.moe_layer_w4(shape or _layer(), w, x, out, ids, wts, ws, 1 << 30, stream=0, check=False)
+
+    for kw in (dict(x=None), dict(out=None), dict(ws=None), dict(router_w=None), dict(w13=None), dict(w13_scales=None),
+               dict(w2=None), dict(w2_scales=None), dict(shared_w13=None), dict(shared_w2_scales=None), dict(w13=4112),
+               dict(shared_w2=4112), dict(norm_w=4104), dict(router_w=4104), dict(w2_scales=4104), dict(bias=4098),
+               dict(x=(1 << 20) + 8), dict(ws=(1 << 22) + 128), dict(out=1 << 20), dict(out=1 << 22), dict(out=(1 << 21) + 1),
+               dict(ids=4098), dict(wts=4098)):
+        assert call(**kw) == moe.MOE_ERR_INVALID_ARG, kw
+    assert moe.load().moe_layer_w4(None, None, None, None, None, None, None, 0, None) == moe.MOE_ERR_INVALID_ARG
