@@ -38,6 +38,7 @@ static int linear_plan(const moe_linear_shape_t& s, int sms, LinearPlan* p) {
   p->mt = p->nc / 2;
   p->TT = (s.M + p->mt - 1) / p->mt;
   p->units = (int64_t)p->RT * p->TT * p->KU;
+  if (p->units > INT_MAX) return MOE_ERR_UNSUPPORTED;
   p->grid = (int)std::min<int64_t>(std::min(sms, kMaxGrid), (p->units + 1) / 2);
   // the parts come first and in one place for every shape: they are zero
   // between calls, the operand blocks behind them are not
@@ -51,7 +52,7 @@ static int linear_plan(const moe_linear_shape_t& s, int sms, LinearPlan* p) {
 }
 
 struct LayerPlan {
-  size_t o_part1, o_part2, o_rstd, o_sig, o_key, o_xop, o_xsf, o_mop, o_msf, total;
+  size_t o_part1, o_part2, o_dot, o_ssq, o_xop, o_xsf, o_mop, o_msf, total;
 };
 
 static int layer_plan(const moe_layer_shape_t& s, LayerPlan* p) {
@@ -68,9 +69,8 @@ static int layer_plan(const moe_layer_shape_t& s, LayerPlan* p) {
   const size_t KC = s.H / 128, tiles = (size_t)std::min(s.E, 16 * s.topk) * (s.I / 128) + s.shared_I / 128;
   p->o_part1 = take((size_t)kMaxGrid * 32 * 128 * 4);
   p->o_part2 = take((size_t)kMaxGrid * 16 * 128 * 4);
-  p->o_rstd = take(16 * 4);
-  p->o_sig = take((size_t)16 * s.E * 4);
-  p->o_key = take((size_t)16 * s.E * 4);
+  p->o_dot = take((size_t)4 * 16 * s.E * 4);
+  p->o_ssq = take(4 * 16 * 4);
   p->o_xop = take(KC * 32 * 128);
   p->o_xsf = take(KC * 512);
   p->o_mop = take(tiles * 32 * 128);
@@ -152,7 +152,7 @@ int moe_linear_w4(const moe_linear_shape_t* shape, const void* x, const void* w_
   p.status = reinterpret_cast<int32_t*>(ws);
   p.xop = ws + pl.o_xop;
   p.xsf = ws + pl.o_xsf;
-  p.ldx = shape->ldx; p.ldo = shape->ldo; p.units = pl.units;
+  p.ldx = shape->ldx; p.ldo = shape->ldo; p.shares = w4::Shares((int)pl.units, pl.grid);
   p.M = shape->M; p.N = shape->N; p.K = shape->K; p.KC = pl.KC; p.KU = pl.KU; p.TT = pl.TT;
   p.out_f32 = shape->out_type == MOE_OUT_F32;
   p.test_withhold = take_withhold();
@@ -218,9 +218,8 @@ int moe_layer_w4(const moe_layer_shape_t* shape, const moe_layer_weights_t* w, c
   p.sync = reinterpret_cast<int32_t*>(ws + 64);
   p.part1 = reinterpret_cast<uint32_t*>(ws + pl.o_part1);
   p.part2 = reinterpret_cast<uint32_t*>(ws + pl.o_part2);
-  p.rstd = reinterpret_cast<float*>(ws + pl.o_rstd);
-  p.sig = reinterpret_cast<float*>(ws + pl.o_sig);
-  p.key = reinterpret_cast<uint32_t*>(ws + pl.o_key);
+  p.dot = reinterpret_cast<float*>(ws + pl.o_dot);
+  p.ssq = reinterpret_cast<float*>(ws + pl.o_ssq);
   p.xop = ws + pl.o_xop; p.xsf = ws + pl.o_xsf;
   p.mop = ws + pl.o_mop; p.msf = ws + pl.o_msf;
   p.ldx = shape->ldx; p.ldo = shape->ldo;

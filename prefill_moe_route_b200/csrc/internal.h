@@ -143,6 +143,26 @@ struct CombineParams {
   int M, H, topk;
 };
 
+#ifdef __CUDACC__
+#define MOE_HD __host__ __device__
+#else
+#define MOE_HD
+#endif
+namespace w4 {
+// `total` units cut into n shares as even as whole units allow, the larger
+// ones first: share c takes [begin(c), begin(c + 1)), unit u is in share of(u).
+struct Shares {
+  int n, base, rem;
+  MOE_HD Shares() {}
+  MOE_HD Shares(int total, int count) : n(count), base(total / count), rem(total % count) {}
+  MOE_HD int begin(int c) const { return c * base + (c < rem ? c : rem); }
+  MOE_HD int of(int u) const {
+    const int big = rem * (base + 1);
+    return u < big ? u / (base + 1) : rem + (u - big) / base;
+  }
+};
+}  // namespace w4
+
 // Parameters of the few-token product y = x W^T on MXFP4 weights (linear.cu).
 struct LinearParams {
   const uint16_t* x;        // bf16, rows ldx elements apart
@@ -153,7 +173,8 @@ struct LinearParams {
   void* out;                // rows ldo elements apart
   uint32_t* part;           // [grid][tokens per tile][128] parts of tiles cut between shares, zero between calls
   int32_t* status;
-  int64_t ldx, ldo, units;  // units = row tiles x token tiles x KU
+  w4::Shares shares;        // of row tiles x token tiles x KU units
+  int64_t ldx, ldo;
   int M, N, K, KC, KU, TT;  // K chunks of 128, units along K, token tiles
   int out_f32;
   int test_withhold;        // test knob: leave the last share's part unpublished
@@ -173,8 +194,7 @@ struct LayerParams {
   int32_t* status;
   int32_t* sync;            // [0] next task, [1] quarters of mid tiles stored; k_layer_head zeroes both
   uint32_t *part1, *part2;  // parts of cut tiles: [grid][gate, up of the tokens][128], [grid][tokens][128]; zero between calls
-  float *rstd, *sig;        // [M], [M][E]
-  uint32_t* key;            // [M][E] selection keys
+  float *dot, *ssq;         // slices of x . router_w [4][16][E], of sum x^2 [4][16]
   uint8_t *xop, *xsf;       // the tokens' operand blocks and scale blocks [H/128]
   uint8_t *mop, *msf;       // mid's, one per GEMM1 tile
   int64_t ldx, ldo;

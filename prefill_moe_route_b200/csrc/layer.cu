@@ -2,13 +2,12 @@
 // two launches: RMS norm, router product, top-k, SwiGLU experts on MXFP4
 // weights with bf16 activations, an always-used shared expert, the residual.
 //
-//   k_layer_head     two experts' router logits a CTA (fp32 products of bf16),
-//                    the norm's statistics on the way, sigmoid and selection
-//                    keys; and the tokens as tensor-core operand columns
-//                    (w4.cuh) of x * norm weight.  The norm's 1 / rms is a factor
-//                    of the token, applied to the sums.
-//   k_layer_experts  one CTA an SM.  Each picks the top k from the keys (the same
-//                    everywhere), then streams weights: GEMM1 over the selected
+//   k_layer_head     the router's logits (bf16 MMAs, nothing rounded) and the
+//                    norm's sums of squares, cut along K; and the tokens as
+//                    tensor-core operand columns (w4.cuh) of x * norm weight.  The
+//                    norm's 1 / rms is a factor of the token, applied to the sums.
+//   k_layer_experts  one CTA an SM.  Each routes the tokens from the logits (the
+//                    same everywhere), then streams weights: GEMM1 over the selected
 //                    experts' gate and up rows, SwiGLU, mid as operand columns
 //                    scaled by the routing weight, and GEMM2, in which the experts
 //                    follow one another along K: one accumulation per 128 rows of
@@ -33,7 +32,11 @@ namespace layer {
 using namespace w4;
 
 constexpr int HEAD_THREADS = 256;
-constexpr int THREADS = 256;       // warps: 0 weights, 1 MMA, 2 operands, 3 routing only, 4-7 sums
+constexpr int HEAD_SLICES = 4;     // CTAs along K of 8 experts' logits
+constexpr int GROUP = 4;           // tokens whose sums one warp keeps
+constexpr int MAX_GROUPS = 4;
+// warps: 0 weights, 1 MMA, 2 operands, 3 routing only, then four a group of tokens for the sums
+constexpr int MAX_THREADS = 128 + 128 * MAX_GROUPS;
 constexpr int STAGES = 5;
 constexpr int SF_SLOTS = 4;        // TMEM scale slots of 16 columns: two weight blocks, two operand blocks
 constexpr int TASKS = 4;           // task ring
@@ -55,38 +58,18 @@ struct Cfg {                       // NC: operand columns, two per token
 struct Smem {
   uint64_t full[STAGES], empty[STAGES], accf[2], acce[2], tfull[TASKS], tempty[TASKS];
   uint32_t tmem;
-  int abort_flag, ndist;
+  int abort_flag;
   int task[TASKS];
   float rstd[MAX_M];
   int ids[MAX_M * kMaxTopk];
   float wts[MAX_M * kMaxTopk];
-  uint8_t mark[kMaxE];
+  uint32_t mask[kMaxE / 32];       // selected experts
   uint16_t dlist[MAX_SLOTS];
 };
 
 template <int NC>
 constexpr int smem_bytes() { return STAGES * Cfg<NC>::STAGE + (int)sizeof(Smem) + 1024; }
 static_assert(smem_bytes<16>() <= 232448 && smem_bytes<32>() <= 232448, "shared memory");
-
-// Sums of R values over the warp, value lane >> (5 - log2 R) in each lane.
-template <int R>
-__device__ __forceinline__ float warp_sums(float (&v)[R]) {
-  const int lane = threadIdx.x & 31;
-  int off = 16;
-#pragma unroll
-  for (int n = R / 2; n >= 1; n /= 2, off /= 2) {
-    const bool up = lane & off;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, off);
-    }
-  }
-  float r = v[0];
-#pragma unroll
-  for (; off >= 1; off /= 2) r += __shfl_xor_sync(0xFFFFFFFFu, r, off);
-  return r;
-}
 
 __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -97,129 +80,198 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
   }
 }
 
-// MT: the tokens' accumulators a thread keeps (M rounded up to a power of two).
-template <int MT>
-__global__ void __launch_bounds__(HEAD_THREADS) k_layer_head(const LayerParams p) {
-  pdl_wait();
-  if (blockIdx.x == 0 && threadIdx.x == 0) { p.sync[0] = 0; p.sync[1] = 0; }
-  pdl_launch_dependents();
-  const int M = p.M, H = p.H, E = p.E, KC = H / 128, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int e0 = 2 * blockIdx.x;
+// D += A B, 16 x 8 x 16, bf16 in, fp32 sums.  (The router product is small: two
+// dependent launches' latency is what counts here, not the tensor rate.)
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
-  // ---- the tokens' operand columns: 16 lanes a chunk of one token
-  for (int kc = blockIdx.x; kc < KC; kc += gridDim.x) {
-    const int t = tid >> 4, g8 = tid & 15, k = kc * 128 + g8 * 8;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (t < M) {
-      unpack8(__ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.ldx + k)), v);
-      if (p.norm_w) {
-        float g[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(p.norm_w + k)), g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= g[i];
-      }
-    }
-    uint32_t am = 0;   // largest magnitude's bits; a NaN's are above an infinity's
-#pragma unroll
-    for (int i = 0; i < 8; ++i) am = max(am, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-    if (t < M) {
-      const int s = split_exp(__uint_as_float(am));
-      const float inv = s == SPLIT_NAN ? __int_as_float(0x7FC00000) : exp2i(-s);
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) split_f16x2(f16x2_of(v[2 * i], v[2 * i + 1], inv), hi[i], lo[i]);
-      uint8_t* tile = p.xop + (int64_t)kc * p.nc * 128;
-      uint8_t* sf = p.xsf + (int64_t)kc * SF_BLOCK;
-      const int mt = p.nc / 2;
-      *reinterpret_cast<uint2*>(tile + tile_byte(t, g8 * 8)) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-      *reinterpret_cast<uint2*>(tile + tile_byte(mt + t, g8 * 8)) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-      if ((g8 & 3) == 0) {
-        sf[sf_byte(t, g8 >> 2)] = static_cast<uint8_t>(split_code_hi(s));
-        sf[sf_byte(mt + t, g8 >> 2)] = static_cast<uint8_t>(split_code_lo(s));
-      }
-    }
-  }
-  if (e0 >= E && blockIdx.x != 0) return;
-
-  // ---- two experts' logits and the sums of squares
-  float dot[2 * MT], ss[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) { dot[2 * i] = dot[2 * i + 1] = 0.0f; ss[i] = 0.0f; }
-  const uint16_t* r0 = p.router_w + (int64_t)min(e0, E - 1) * H;
-  const uint16_t* r1 = p.router_w + (int64_t)min(e0 + 1, E - 1) * H;
-#pragma unroll 2
-  for (int k = tid * 8; k < H; k += HEAD_THREADS * 8) {
-    float a[8], b[8];
-    unpack8(__ldg(reinterpret_cast<const uint4*>(r0 + k)), a);
-    unpack8(__ldg(reinterpret_cast<const uint4*>(r1 + k)), b);
+// One 128-K chunk of the tokens as operand columns: 16 lanes a token.
+__device__ __forceinline__ void split_chunk(const LayerParams& p, int kc) {
+  const int t = threadIdx.x >> 4, g8 = threadIdx.x & 15, k = kc * 128 + g8 * 8;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (t < p.M) {
+    unpack8(__ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.ldx + k)), v);
     if (p.norm_w) {
       float g[8];
       unpack8(__ldg(reinterpret_cast<const uint4*>(p.norm_w + k)), g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) { a[i] *= g[i]; b[i] *= g[i]; }   // exact: 8-bit significands
-    }
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      if (t >= M) break;
-      float v[8];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.ldx + k)), v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dot[2 * t] = fmaf(v[i], a[i], dot[2 * t]);
-        dot[2 * t + 1] = fmaf(v[i], b[i], dot[2 * t + 1]);
-        ss[t] = fmaf(v[i], v[i], ss[t]);
-      }
+      for (int i = 0; i < 8; ++i) v[i] *= g[i];
     }
   }
-  __shared__ float sd[8][2 * MT], sq[8][MT];
-  const float d = warp_sums(dot), q = warp_sums(ss);
-  if (lane % (32 / (2 * MT)) == 0) sd[warp][lane / (32 / (2 * MT))] = d;
-  if (lane % (32 / MT) == 0) sq[warp][lane / (32 / MT)] = q;
-  __syncthreads();
-  if (tid < 2 * M) {
-    const int t = tid >> 1, e = e0 + (tid & 1);
-    float dsum = 0.0f, qsum = 0.0f;
+  uint32_t am = 0;   // largest magnitude's bits; a NaN's are above an infinity's
 #pragma unroll
-    for (int w = 0; w < 8; ++w) { dsum += sd[w][tid]; qsum += sq[w][t]; }
-    const float rstd = p.norm_w ? 1.0f / sqrtf(qsum / (float)H + p.eps) : 1.0f;
-    if (e < E) {
-      const float sg = sigmoid_spec(dsum * rstd);
-      p.sig[t * E + e] = sg;
-      p.key[t * E + e] = float_order_key(p.bias ? __fadd_rn(sg, __ldg(p.bias + e)) : sg);
-    }
-    if (blockIdx.x == 0 && (tid & 1) == 0) p.rstd[t] = rstd;
+  for (int i = 0; i < 8; ++i) am = max(am, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+  am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+  if (t >= p.M) return;
+  const int s = split_exp(__uint_as_float(am));
+  const float inv = s == SPLIT_NAN ? __int_as_float(0x7FC00000) : exp2i(-s);
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split_f16x2(f16x2_of(v[2 * i], v[2 * i + 1], inv), hi[i], lo[i]);
+  uint8_t* tile = p.xop + (int64_t)kc * p.nc * 128;
+  uint8_t* sf = p.xsf + (int64_t)kc * SF_BLOCK;
+  const int mt = p.nc / 2;
+  *reinterpret_cast<uint2*>(tile + tile_byte(t, g8 * 8)) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+  *reinterpret_cast<uint2*>(tile + tile_byte(mt + t, g8 * 8)) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+  if ((g8 & 3) == 0) {
+    sf[sf_byte(t, g8 >> 2)] = static_cast<uint8_t>(split_code_hi(s));
+    sf[sf_byte(mt + t, g8 >> 2)] = static_cast<uint8_t>(split_code_lo(s));
   }
 }
 
-// The top k of one token from its selection keys, a warp: k rounds, a tie
-// going to the lower expert; weights as in route_token_warp.
-template <int KPER>
-__device__ __forceinline__ void pick(const uint32_t* keys, const float* sig, int E, int k, float scale, int* ids,
-                                     float* wts) {
-  const int lane = threadIdx.x & 31;
-  uint32_t key[KPER];
-  float sg[KPER];
+// CTAs [0, groups * HEAD_SLICES): the logits of 8 experts over a slice of K, a
+// warp every 32nd block of 32 K.  The other CTAs: one operand chunk each.
+// A thread holds 8 consecutive K of token g, of token g + 8 and of expert g (g =
+// lane / 4): two MMAs' fragments with K permuted the same way on both sides.
+// The norm weight multiplies the router weight; the product of two 8-bit
+// significands is two bf16 exactly, so nothing is rounded before the sums.
+__global__ void __launch_bounds__(HEAD_THREADS, 2) k_layer_head(const LayerParams p) {
+  constexpr int BATCH = 6;   // blocks in flight
+  pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) { p.sync[0] = 0; p.sync[1] = 0; }
+  pdl_launch_dependents();
+  const int M = p.M, H = p.H, E = p.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nlogit = (E + 7) / 8 * HEAD_SLICES;
+  if (blockIdx.x >= nlogit) { split_chunk(p, blockIdx.x - nlogit); return; }
+  const int eg = blockIdx.x / HEAD_SLICES, slice = blockIdx.x % HEAD_SLICES;
+  const int g = lane >> 2, kq = (lane & 3) * 8, nblk = H / 32;
+  const bool e_ok = eg * 8 + g < E, t0 = g < M, t1 = g + 8 < M, norm = p.norm_w != nullptr;
+  const uint16_t* wr = p.router_w + (int64_t)(e_ok ? eg * 8 + g : 0) * H + kq;
+  const uint16_t* x0 = p.x + (int64_t)(t0 ? g : 0) * p.ldx + kq;
+  const uint16_t* x1 = p.x + (int64_t)(t1 ? g + 8 : 0) * p.ldx + kq;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  float d[4] = {0.f, 0.f, 0.f, 0.f}, ss0 = 0.0f, ss1 = 0.0f;
+  for (int b0 = slice * 8 + warp; b0 < nblk; b0 += 8 * HEAD_SLICES * BATCH) {
+    uint4 w[BATCH], gw[BATCH], xa[BATCH], xb[BATCH];
 #pragma unroll
-  for (int i = 0; i < KPER; ++i) {
-    const int e = lane + 32 * i;
-    key[i] = e < E ? __ldcg(keys + e) : 0u;
-    sg[i] = e < E ? __ldcg(sig + e) : 0.0f;
+    for (int i = 0; i < BATCH; ++i) {
+      const int b = b0 + i * 8 * HEAD_SLICES;
+      const bool in = b < nblk;
+      w[i] = in && e_ok ? __ldg(reinterpret_cast<const uint4*>(wr + b * 32)) : zero;
+      gw[i] = in && norm ? __ldg(reinterpret_cast<const uint4*>(p.norm_w + kq + b * 32)) : zero;
+      xa[i] = in && t0 ? __ldg(reinterpret_cast<const uint4*>(x0 + b * 32)) : zero;
+      xb[i] = in && t1 ? __ldg(reinterpret_cast<const uint4*>(x1 + b * 32)) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const uint32_t a[4] = {xa[i].x, xa[i].y, xa[i].z, xa[i].w}, c[4] = {xb[i].x, xb[i].y, xb[i].z, xb[i].w};
+      uint32_t bh[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      if (norm) {
+        float wf[8], gf[8];
+        unpack8(w[i], wf);
+        unpack8(gw[i], gf);
+        uint32_t bl[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float q0 = wf[2 * j] * gf[2 * j], q1 = wf[2 * j + 1] * gf[2 * j + 1];
+          bh[j] = pack_bf16x2(q0, q1);
+          bl[j] = pack_bf16x2(q0 - __uint_as_float(bh[j] << 16), q1 - __uint_as_float(bh[j] & 0xFFFF0000u));
+        }
+        mma_16816(d, a[0], c[0], a[1], c[1], bl[0], bl[1]);
+        mma_16816(d, a[2], c[2], a[3], c[3], bl[2], bl[3]);
+        if (eg == 0) {
+          float f[8];
+          unpack8(xa[i], f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ss0 = fmaf(f[j], f[j], ss0);
+          unpack8(xb[i], f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ss1 = fmaf(f[j], f[j], ss1);
+        }
+      }
+      mma_16816(d, a[0], c[0], a[1], c[1], bh[0], bh[1]);
+      mma_16816(d, a[2], c[2], a[3], c[3], bh[2], bh[3]);
+    }
   }
+  __shared__ float sd[8][16][8], sq[8][16];
+  *reinterpret_cast<float2*>(&sd[warp][g][(lane & 3) * 2]) = make_float2(d[0], d[1]);
+  *reinterpret_cast<float2*>(&sd[warp][g + 8][(lane & 3) * 2]) = make_float2(d[2], d[3]);
+  if (norm && eg == 0) {
+#pragma unroll
+    for (int o = 1; o <= 2; o *= 2) {
+      ss0 += __shfl_xor_sync(0xFFFFFFFFu, ss0, o);
+      ss1 += __shfl_xor_sync(0xFFFFFFFFu, ss1, o);
+    }
+    if ((lane & 3) == 0) { sq[warp][g] = ss0; sq[warp][g + 8] = ss1; }
+  }
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    const int t = threadIdx.x >> 3, e = eg * 8 + (threadIdx.x & 7);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += sd[i][t][threadIdx.x & 7];
+    if (t < M && e < E) p.dot[((int64_t)slice * MAX_M + t) * E + e] = sum;
+  } else if (norm && eg == 0 && threadIdx.x < 128 + 16) {
+    const int t = threadIdx.x - 128;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += sq[i][t];
+    p.ssq[slice * MAX_M + t] = sum;
+  }
+}
+
+// Routes token t with one warp from its logits' slices: sigmoid, the top k of
+// sigmoid + bias in k rounds (a tie going to the lower expert), weights as in
+// route_token_warp.  Returns the norm's factor of the token.  Every CTA runs
+// this once, cold, so the code is kept short (the sigmoids in a loop through
+// `scratch`, 64 KPER words of the warp's own).
+template <int KPER>
+__device__ __forceinline__ float pick(const LayerParams& p, int t, int* ids, float* wts, uint32_t* mask,
+                                      uint32_t* scratch) {
+  const int lane = threadIdx.x & 31, E = p.E, k = p.topk;
+  uint32_t* skey = scratch;                                     // [KPER][32] bias, then selection keys
+  float* ssig = reinterpret_cast<float*>(scratch + 32 * KPER);  // [KPER][32] x . router_w, then sigmoids
+  float rstd = 1.0f;
+  {
+    float part[HEAD_SLICES][KPER], ssq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < KPER; ++i) {
+      const int e = lane + 32 * i;
+#pragma unroll
+      for (int q = 0; q < HEAD_SLICES; ++q) part[q][i] = e < E ? __ldcg(p.dot + (q * MAX_M + t) * E + e) : 0.0f;
+      skey[i * 32 + lane] = p.bias && e < E ? __float_as_uint(__ldg(p.bias + e)) : 0u;
+    }
+    if (p.norm_w) {
+#pragma unroll
+      for (int q = 0; q < HEAD_SLICES; ++q) ssq += __ldcg(p.ssq + q * MAX_M + t);
+      rstd = 1.0f / sqrtf(ssq / (float)p.H + p.eps);
+    }
+#pragma unroll
+    for (int i = 0; i < KPER; ++i) {
+      float l = part[0][i];
+#pragma unroll
+      for (int q = 1; q < HEAD_SLICES; ++q) l += part[q][i];
+      ssig[i * 32 + lane] = l;
+    }
+  }
+#pragma unroll 1
+  for (int i = 0; i < KPER; ++i) {
+    const float sg = sigmoid_spec(ssig[i * 32 + lane] * rstd);
+    ssig[i * 32 + lane] = sg;
+    const float sc = p.bias ? __fadd_rn(sg, __uint_as_float(skey[i * 32 + lane])) : sg;
+    skey[i * 32 + lane] = lane + 32 * i < E ? float_order_key(sc) : 0u;
+  }
+  __syncwarp();
+  uint32_t key[KPER];
+#pragma unroll
+  for (int i = 0; i < KPER; ++i) key[i] = skey[i * 32 + lane];
   float denom = 0.0f, mine = 0.0f;
   int id = 0;
 #pragma unroll 1
   for (int j = 0; j < k; ++j) {
     uint32_t best = key[0];
     int bi = 0;
-    float bs = sg[0];
 #pragma unroll
     for (int i = 1; i < KPER; ++i)
-      if (key[i] > best) { best = key[i]; bi = i; bs = sg[i]; }
+      if (key[i] > best) { best = key[i]; bi = i; }
     const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
     const int e = (int)__reduce_min_sync(0xFFFFFFFFu, best == top ? (uint32_t)(lane + 32 * bi) : 0xFFFFFFFFu);
-    const float s = __shfl_sync(0xFFFFFFFFu, bs, e & 31);
+    const float s = ssig[e];
 #pragma unroll
     for (int i = 0; i < KPER; ++i)
       if (lane + 32 * i == e) key[i] = 0u;   // taken (below every key of a number or a NaN)
@@ -228,12 +280,17 @@ __device__ __forceinline__ void pick(const uint32_t* keys, const float* sig, int
   }
   if (lane < k) {
     ids[lane] = id;
-    wts[lane] = __fmul_rn(__fdiv_rn(mine, denom), scale);
+    wts[lane] = __fmul_rn(__fdiv_rn(mine, denom), p.scale);
+    atomicOr(mask + (id >> 5), 1u << (id & 31));
   }
+  return rstd;
 }
 
-template <int NC>
-__global__ void __launch_bounds__(THREADS, 1)
+// NC: operand columns; TG: tokens a warp's group holds (1 and 2 for as many
+// tokens, else GROUP): the sums of a tile are spread over four warps a group, so
+// that the code is short and a tile's epilogue takes as long for 16 tokens as for 4.
+template <int NC, int TG>
+__global__ void __launch_bounds__(TG == GROUP ? (NC == 32 ? MAX_THREADS : 384) : 256, 1)
 k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant__ CUtensorMap tmW2,
                 const __grid_constant__ CUtensorMap tmS13, const __grid_constant__ CUtensorMap tmS2, const LayerParams p) {
   using C = Cfg<NC>;
@@ -249,10 +306,11 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int M = p.M, E = p.E, topk = p.topk, KC = p.H / 128, HT = p.H / 128, J = p.I / 128, JS = p.S / 128;
 
+  const int groups = (M + TG - 1) / TG, epi_warps = 4 * groups;   // the block has 4 + epi_warps warps
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) { mbar_init(&S.full[s], 2); mbar_init(&S.empty[s], 1); }
-    for (int b = 0; b < 2; ++b) { mbar_init(&S.accf[b], 1); mbar_init(&S.acce[b], 4); }
-    for (int t = 0; t < TASKS; ++t) { mbar_init(&S.tfull[t], 1); mbar_init(&S.tempty[t], 6); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&S.accf[b], 1); mbar_init(&S.acce[b], epi_warps); }
+    for (int t = 0; t < TASKS; ++t) { mbar_init(&S.tfull[t], 1); mbar_init(&S.tempty[t], 2 + epi_warps); }
     S.abort_flag = 0;
     fence_mbar_init();
   }
@@ -261,46 +319,44 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     if (JS) { tma_prefetch_desc(&tmS13); tma_prefetch_desc(&tmS2); }
   }
   if (warp == 4) { tmem_alloc(&S.tmem, C::TMEM_COLS); tmem_relinquish(); }
-  for (int e = threadIdx.x; e < E; e += THREADS) S.mark[e] = 0;
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + kMaxE / 32) S.mask[threadIdx.x - 64] = 0u;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   pdl_wait();   // k_layer_head is done
   pdl_launch_dependents();
   int ticket = 0;
   if (threadIdx.x == 0) ticket = atomicAdd(p.sync, 1);   // in flight while routing runs
-  for (int t = warp; t < M; t += THREADS / 32) {
-    if (E <= 256) pick<8>(p.key + t * E, p.sig + t * E, E, topk, p.scale, S.ids + t * topk, S.wts + t * topk);
-    else pick<kMaxE / 32>(p.key + t * E, p.sig + t * E, E, topk, p.scale, S.ids + t * topk, S.wts + t * topk);
+  if (warp < M) {   // one token a warp: there are at least M warps
+    uint32_t* scratch = reinterpret_cast<uint32_t*>(abuf) + warp * 2 * kMaxE;   // in the idle ring
+    const float r = E <= 256 ? pick<8>(p, warp, S.ids + warp * topk, S.wts + warp * topk, S.mask, scratch)
+                             : pick<kMaxE / 32>(p, warp, S.ids + warp * topk, S.wts + warp * topk, S.mask, scratch);
+    if (lane == 0) S.rstd[warp] = r;
+    fence_proxy_async_smem();   // the ring's next writers are asynchronous copies
   }
-  if (threadIdx.x < M) S.rstd[threadIdx.x] = __ldcg(p.rstd + threadIdx.x);
   __syncthreads();
-  for (int q = threadIdx.x; q < M * topk; q += THREADS) {
-    S.mark[S.ids[q]] = 1;
-    if (blockIdx.x == 0) {
+  // the selected experts, ascending: prefix counts of the mask's words, a thread an expert
+  const uint32_t mword = lane < kMaxE / 32 ? S.mask[lane] : 0u;
+  int ndist;
+  const int before = warp_exclusive_scan(__popc(mword), &ndist);
+  for (int i = warp; i < (E + 31) / 32; i += blockDim.x / 32) {
+    const uint32_t m = __shfl_sync(0xFFFFFFFFu, mword, i);
+    const int n = __shfl_sync(0xFFFFFFFFu, before, i) + __popc(m & ((1u << lane) - 1u));
+    if ((m >> lane) & 1u) S.dlist[n] = static_cast<uint16_t>(32 * i + lane);
+  }
+  if (blockIdx.x == 0)
+    for (int q = threadIdx.x; q < M * topk; q += blockDim.x) {
       if (p.ids_out) p.ids_out[q] = S.ids[q];
       if (p.wts_out) p.wts_out[q] = S.wts[q];
     }
-  }
   __syncthreads();
-  if (warp == 0) {   // the selected experts, ascending
-    int n = 0;
-    for (int e = lane; e < (E + 31) / 32 * 32; e += 32) {
-      const bool on = e < E && S.mark[e];
-      const uint32_t m = __ballot_sync(0xFFFFFFFFu, on);
-      if (on) S.dlist[n + __popc(m & ((1u << lane) - 1u))] = static_cast<uint16_t>(e);
-      n += __popc(m);
-    }
-    if (lane == 0) S.ndist = n;
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, S.tmem, 0);
   const uint64_t deadline = globaltimer() + p.timeout_ns;
   // GEMM1: tile i (a gate and an up tile; the shared expert's first) is chunk i
   // of GEMM2's K.  A unit is 128 K of a GEMM1 tile or two chunks of a GEMM2 tile.
-  const int tiles1 = JS + S.ndist * J, CU = (tiles1 + 1) / 2;
-  const int64_t U1 = (int64_t)tiles1 * KC, U2 = (int64_t)HT * CU;
-  const int G = gridDim.x;
-  const int S1 = (int)min((int64_t)G, (U1 + MIN_SHARE - 1) / MIN_SHARE), S2 = (int)min((int64_t)G, (U2 + MIN_SHARE - 1) / MIN_SHARE);
+  const int tiles1 = JS + ndist * J, CU = (tiles1 + 1) / 2;
+  const int U1 = tiles1 * KC, U2 = HT * CU, G = gridDim.x;
+  const Shares sh1(U1, min(G, (U1 + MIN_SHARE - 1) / MIN_SHARE)), sh2(U2, min(G, (U2 + MIN_SHARE - 1) / MIN_SHARE));
   struct Where { int e, j, iw; bool shared; };
   auto where = [&](int i) -> Where {
     if (i < JS) return {0, i, JS, true};
@@ -313,16 +369,12 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     atomicCAS(p.status + 2, 0, (int)(0x80000000u | (9u << 24) | ((unsigned)site << 20) | (blockIdx.x & 0xFFFu)));
   };
   auto drain = [&]() { const uint64_t until = globaltimer() + 2000000ull; while (globaltimer() < until) { } };
-  // Ticket -> product (1, 2; 0: no more tasks), its units [u0, u1), units per tile, share, shares.
-  struct Task { int gemm, share, shares, len; int64_t total, u0, u1; };
-  auto task_of = [&](int t) -> Task {
-    Task k;
-    if (t < S1) k = {1, S1 - 1 - t, S1, KC, U1, 0, 0};   // a share waits for later ones: they are drawn before it
-    else if (t < S1 + S2) k = {2, S2 - 1 - (t - S1), S2, CU, U2, 0, 0};
-    else return {0, 0, 1, 1, 0, 0, 0};
-    k.u0 = share_begin(k.total, k.shares, k.share);
-    k.u1 = share_begin(k.total, k.shares, k.share + 1);
-    return k;
+  // Ticket -> product (1, 2; 0: no more tasks), its share and units [u0, u1), units per tile.
+  struct Task { int gemm, share, len, u0, u1; };
+  auto task_of = [&](int t) -> Task {   // a share waits for later ones: they are drawn before it
+    if (t < sh1.n) { const int c = sh1.n - 1 - t; return {1, c, KC, sh1.begin(c), sh1.begin(c + 1)}; }
+    if (t < sh1.n + sh2.n) { const int c = sh1.n + sh2.n - 1 - t; return {2, c, CU, sh2.begin(c), sh2.begin(c + 1)}; }
+    return {0, 0, 1, 0, 0};
   };
   // The other roles take the tasks in the order that the weight stream drew them.
   auto next_task = [&](int n, Task* k) -> bool {   // a whole warp
@@ -348,9 +400,9 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
         const Task k = task_of(ticket);
         if (!k.gemm) break;
         ticket = atomicAdd(p.sync, 1);
-        int tile = static_cast<int>(k.u0 / k.len), i = static_cast<int>(k.u0 - (int64_t)tile * k.len);
+        int tile = k.u0 / k.len, i = k.u0 - tile * k.len;
         Where w = where(k.gemm == 1 ? tile : 0);
-        for (int64_t u = k.u0; u < k.u1; ++u) {
+        for (int u = k.u0; u < k.u1; ++u) {
           if (!mbar_wait(&S.empty[st], ph ^ 1, deadline, abort_flag)) { fail(3); ok = false; break; }
           uint8_t* a = abuf + st * C::A_BYTES;
           uint8_t* sf = asf + st * C::SF_BYTES;
@@ -391,9 +443,9 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     bool ok = true;
     Task k;
     for (int n = 0; ok && (ok = next_task(n, &k)); ++n) {
-      int i = static_cast<int>(k.u0 % k.len);
+      int i = k.u0 % k.len;
       bool first = true;
-      const int nu = static_cast<int>(k.u1 - k.u0);
+      const int nu = k.u1 - k.u0;
       const bool one = k.gemm == 1;
       for (int x = 0; x < nu; ++x) {
         const int b = seg & 1;
@@ -454,9 +506,9 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     fence_proxy_async_global();   // k_layer_head's stores, read by bulk copies
     for (int n = 0; ok && (ok = next_task(n, &k)); ++n) {
       if (k.gemm == 2 && !mid_ready) {
-        // every GEMM1 tile's four warps have stored their quarter of mid
+        // every GEMM1 tile's warps have stored their piece of mid
         uint32_t spins = 0;
-        while (ld_acquire_gpu(p.sync + 1) < 4 * tiles1) {
+        while (ld_acquire_gpu(p.sync + 1) < epi_warps * tiles1) {
           if ((++spins & 15u) == 0 && (*abort_flag || globaltimer() > deadline)) { fail(6); ok = false; break; }
         }
         if (!ok) break;
@@ -465,8 +517,8 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
         mid_ready = true;
       }
       if (lane == 0) {
-        int i = static_cast<int>(k.u0 % k.len);
-        for (int64_t u = k.u0; u < k.u1; ++u) {
+        int i = k.u0 % k.len;
+        for (int u = k.u0; u < k.u1; ++u) {
           if (!mbar_wait(&S.empty[st], ph ^ 1, deadline, abort_flag)) { fail(7); ok = false; break; }
           const int nk = k.gemm == 1 ? 1 : min(2, tiles1 - 2 * i);
           const int64_t blk = k.gemm == 1 ? i : 2 * i;
@@ -485,14 +537,17 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------ sums
-    const int q = warp - 4, row = 32 * q + lane;   // TMEM lane quarter = warp % 4
-    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    const int q = warp & 3, row = 32 * q + lane;   // TMEM lane quarter = warp % 4
+    const int t0 = (warp - 4) / 4 * TG;            // this warp's tokens t0 .. t0 + TG - 1
+    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q) << 16) + t0;
     int seg = 0;
     bool ok = true;
     Task k;
-    // adds the later shares' parts [share + 1, c1] of NV values per row, in K order, to v
-    auto gather = [&](uint32_t* part, int share, int c1, auto& v, auto nv_const, auto live) -> bool {
-      constexpr int NV = decltype(nv_const)::value, CB = 64 / NV;
+    // Adds the later shares' parts [share + 1, c1] of NV values per row, in K
+    // order, to v; value i is token t0 + i % TG's.
+    auto live = [&](int i) { return t0 + (i & (TG - 1)) < M; };
+    auto gather = [&](uint32_t* part, int share, int c1, auto& v, auto nv_const) -> bool {
+      constexpr int NV = decltype(nv_const)::value, CB = NV >= 2 ? 32 / NV : 16;   // parts per batch
 #pragma unroll 1
       for (int cb = share + 1; cb <= c1; cb += CB) {
         uint32_t w[CB][NV];
@@ -501,9 +556,9 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
           bool all = true;
 #pragma unroll
           for (int c = 0; c < CB; ++c) {
-            const uint32_t* src = part + (int64_t)min(cb + c, c1) * (NV * 128) + row;
+            const uint32_t* src = part + min(cb + c, c1) * (MAX_GROUPS * NV * 128);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) w[c][i] = live(i) ? part_peek(src + i * 128) : 1u;
+            for (int i = 0; i < NV; ++i) w[c][i] = live(i) && cb + c <= c1 ? part_peek(src + i * 128) : 1u;
           }
 #pragma unroll
           for (int c = 0; c < CB; ++c)
@@ -515,7 +570,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
 #pragma unroll
         for (int c = 0; c < CB; ++c) {
           if (cb + c > c1) break;
-          uint32_t* src = part + (int64_t)(cb + c) * (NV * 128) + row;
+          uint32_t* src = part + (cb + c) * (MAX_GROUPS * NV * 128);
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
             v[i] += part_value(w[c][i]);
@@ -525,106 +580,104 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
       }
       return true;
     };
+    // [share][group][value][row]
+    uint32_t* part1 = p.part1 + t0 * 2 * 128 + row;
+    uint32_t* part2 = p.part2 + t0 * 128 + row;
     for (int n = 0; ok && next_task(n, &k); ++n) {
-      for (int64_t u = k.u0; u < k.u1 && ok; ++seg) {
-        const int tile = static_cast<int>(u / k.len);
-        const int64_t t0 = (int64_t)tile * k.len, t1 = t0 + k.len, ue = min(t1, k.u1);
-        const bool mine = u == t0;   // this share starts the tile and so finishes it
-        const int c1 = mine ? share_of(k.total, k.shares, t1 - 1) : k.share;
+      for (int u = k.u0; u < k.u1 && ok; ++seg) {
+        const int tile = u / k.len, tb = tile * k.len, te = tb + k.len, ue = min(te, k.u1);
+        const bool mine = u == tb;   // this share starts the tile and so finishes it
+        const int c1 = mine ? (k.gemm == 1 ? sh1 : sh2).of(te - 1) : k.share;
         const int b = seg & 1;
         if (!mbar_wait(&S.accf[b], (seg >> 1) & 1, deadline, abort_flag)) { fail(9); ok = false; break; }
         __syncwarp();
         tc_fence_after();
         const uint32_t acc = tl + b * 2 * NC;
-        // sum over a token's two columns
-        auto read = [&](uint32_t col, float* v) {
-          float a[16], c[16];
-          tmem_ld16(col, a);
-          if constexpr (NC == 32) tmem_ld16(col + MT, c);
+        float v[2 * TG];   // gate of token t0 + t, then up; or out
+        {
+          float a[TG], c[TG], d[TG], e[TG];   // a token's two columns, of each accumulator
+          tmem_ld(acc, a);
+          tmem_ld(acc + MT, c);
+          if (k.gemm == 1) {
+            tmem_ld(acc + NC, d);
+            tmem_ld(acc + NC + MT, e);
+          }
           tmem_ld_wait();
 #pragma unroll
-          for (int t = 0; t < MT; ++t) v[t] = a[t] + (NC == 32 ? c[t] : a[(MT + t) & 15]);
-        };
-        auto release = [&]() {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&S.acce[b]);
-        };
+          for (int t = 0; t < TG; ++t) { v[t] = a[t] + c[t]; v[TG + t] = d[t] + e[t]; }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.acce[b]);
         if (k.gemm == 1) {
-          float v[2 * MT];   // gate of token t, then up
-          read(acc, v);
-          read(acc + NC, v + MT);
-          release();
-          auto live = [&](int i) { return (i & (MT - 1)) < M; };
           if (!mine) {
-            uint32_t* dst = p.part1 + (int64_t)k.share * (2 * MT * 128) + row;
+            uint32_t* dst = part1 + k.share * (MAX_GROUPS * 2 * TG * 128);
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i)
+            for (int i = 0; i < 2 * TG; ++i)
               if (live(i)) part_put(dst + i * 128, v[i]);
           } else {
-            if (!gather(p.part1, k.share, c1, v, std::integral_constant<int, 2 * MT>(), live)) { ok = false; break; }
             const Where w = where(tile);
+            float wt[TG];   // routing weights; 0: the token did not choose the expert
+#pragma unroll
+            for (int t = 0; t < TG; ++t) wt[t] = w.shared && live(t) ? 1.0f : 0.0f;
+            if (!w.shared) {
+#pragma unroll 1
+              for (int j = 0; j < topk; ++j)
+#pragma unroll
+                for (int t = 0; t < TG; ++t)
+                  if (live(t) && S.ids[(t0 + t) * topk + j] == w.e) wt[t] = S.wts[(t0 + t) * topk + j];
+            }
+            if (!gather(part1, k.share, c1, v, std::integral_constant<int, 2 * TG>())) { ok = false; break; }
+            float m[TG];
+            int s[TG];
+#pragma unroll
+            for (int t = 0; t < TG; ++t) {
+              const float r = S.rstd[min(t0 + t, MAX_M - 1)], g = v[t] * r, h = v[TG + t] * r;
+              // past -80 the quotient's divisor would overflow; there silu(g) is g e^g
+              const float x = __expf(g < -80.0f ? g : -g);
+              const float silu = g < -80.0f ? g * x : __fdividef(g, 1.0f + x);
+              m[t] = wt[t] != 0.0f ? wt[t] * (silu * h) : 0.0f;   // a select: an absent token's sums count for nothing
+              // a block of 32 rows is this warp's rows of the tile
+              s[t] = split_exp(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m[t]) & 0x7FFFFFFFu)));
+              m[t] *= s[t] == SPLIT_NAN ? __int_as_float(0x7FC00000) : exp2i(-s[t]);
+            }
             uint8_t* dst = p.mop + (int64_t)tile * C::B_TILE;
             uint8_t* sf = p.msf + (int64_t)tile * SF_BLOCK;
 #pragma unroll
-            for (int t = 0; t < MT; t += 2) {
-              if (t >= M) break;
-              float m[2];
-              int s[2];
-#pragma unroll
-              for (int o = 0; o < 2; ++o) {
-                const int tt = t + o;
-                float wt = tt < M && w.shared ? 1.0f : 0.0f;
-                if (tt < M && !w.shared)
-                  for (int j = 0; j < topk; ++j)
-                    if (S.ids[tt * topk + j] == w.e) wt = S.wts[tt * topk + j];
-                float x = 0.0f;   // a token that did not choose the expert: zero, whatever its sums
-                if (tt < M && (w.shared || wt != 0.0f)) {
-                  const float r = S.rstd[tt], g = v[tt] * r, h = v[MT + tt] * r;
-                  x = wt * (g / (1.0f + expf(-g)) * h);
-                }
-                const uint32_t am = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x) & 0x7FFFFFFFu);
-                s[o] = split_exp(__uint_as_float(am));
-                m[o] = x * (s[o] == SPLIT_NAN ? __int_as_float(0x7FC00000) : exp2i(-s[o]));
-              }
+            for (int t = 0; t < TG; t += 2) {
               uint32_t hi, lo;
-              split_f16x2(f16x2_of(m[0], m[1], 1.0f), hi, lo);
+              split_f16x2(f16x2_of(m[t], m[TG > 1 ? t + 1 : t], 1.0f), hi, lo);
 #pragma unroll
-              for (int o = 0; o < 2; ++o) {
-                const int tt = t + o;
-                if (tt >= M) break;
-                dst[tile_byte(tt, row)] = static_cast<uint8_t>(hi >> (8 * o));
-                dst[tile_byte(MT + tt, row)] = static_cast<uint8_t>(lo >> (8 * o));
-                if (lane == 0) {
-                  sf[sf_byte(tt, q)] = static_cast<uint8_t>(split_code_hi(s[o]));
-                  sf[sf_byte(MT + tt, q)] = static_cast<uint8_t>(split_code_lo(s[o]));
+              for (int o = 0; o < min(2, TG); ++o)
+                if (live(t + o)) {
+                  dst[tile_byte(t0 + t + o, row)] = static_cast<uint8_t>(hi >> (8 * o));
+                  dst[tile_byte(MT + t0 + t + o, row)] = static_cast<uint8_t>(lo >> (8 * o));
+                  if (lane == 0) {
+                    sf[sf_byte(t0 + t + o, q)] = static_cast<uint8_t>(split_code_hi(s[t + o]));
+                    sf[sf_byte(MT + t0 + t + o, q)] = static_cast<uint8_t>(split_code_lo(s[t + o]));
+                  }
                 }
-              }
             }
             __threadfence();
             __syncwarp();
             if (lane == 0 && !(p.test_withhold && tile == 0)) atomicAdd(p.sync + 1, 1);
           }
         } else {
-          float v[MT];
-          read(acc, v);
-          release();
-          auto live = [&](int i) { return i < M; };
           if (!mine) {
-            uint32_t* dst = p.part2 + (int64_t)k.share * (MT * 128) + row;
+            uint32_t* dst = part2 + k.share * (MAX_GROUPS * TG * 128);
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+            for (int i = 0; i < TG; ++i)
               if (live(i)) part_put(dst + i * 128, v[i]);
           } else {
-            if (!gather(p.part2, k.share, c1, v, std::integral_constant<int, MT>(), live)) { ok = false; break; }
             const int h = tile * 128 + row;
+            float r[TG];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-              if (t >= M) break;
-              float y = v[t];
-              if (p.residual) y += __uint_as_float((uint32_t)__ldg(p.x + (int64_t)t * p.ldx + h) << 16);
-              p.out[(int64_t)t * p.ldo + h] = bf16_bits(y);
-            }
+            for (int t = 0; t < TG; ++t)
+              r[t] = p.residual && live(t) ? __uint_as_float((uint32_t)__ldg(p.x + (t0 + t) * p.ldx + h) << 16) : 0.0f;
+            if (!gather(part2, k.share, c1, v, std::integral_constant<int, TG>())) { ok = false; break; }
+#pragma unroll
+            for (int t = 0; t < TG; ++t)
+              if (live(t)) p.out[(t0 + t) * p.ldo + h] = bf16_bits(v[t] + r[t]);
           }
         }
         u = ue;
@@ -654,37 +707,34 @@ static cudaLaunchConfig_t config(int grid, int threads, int smem, cudaStream_t s
   return cfg;
 }
 
-template <int NC>
+template <int NC, int TG>
 static cudaError_t launch_experts(const CUtensorMap* m, const LayerParams& p, int grid, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};   // devices on which the kernel may take its shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
-    e = cudaFuncSetAttribute(k_layer_experts<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NC>());
+    e = cudaFuncSetAttribute(k_layer_experts<NC, TG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NC>());
     if (e != cudaSuccess) return e;
     if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = config(grid, THREADS, smem_bytes<NC>(), st, &attr);
-  return cudaLaunchKernelEx(&cfg, k_layer_experts<NC>, m[0], m[1], m[2], m[3], p);
+  const cudaLaunchConfig_t cfg = config(grid, 128 + 128 * ((p.M + TG - 1) / TG), smem_bytes<NC>(), st, &attr);
+  return cudaLaunchKernelEx(&cfg, k_layer_experts<NC, TG>, m[0], m[1], m[2], m[3], p);
 }
 
 }  // namespace layer
 
 cudaError_t launch_layer_w4(const CUtensorMap* maps, const LayerParams& p, int sms, cudaStream_t st) {
   using namespace layer;
-  const int head = std::max((p.E + 1) / 2, std::min(p.H / 128, sms));
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = config(head, HEAD_THREADS, 0, st, &attr);
-  cudaError_t e;
-  if (p.M == 1) e = cudaLaunchKernelEx(&cfg, k_layer_head<1>, p);
-  else if (p.M == 2) e = cudaLaunchKernelEx(&cfg, k_layer_head<2>, p);
-  else if (p.M <= 4) e = cudaLaunchKernelEx(&cfg, k_layer_head<4>, p);
-  else if (p.M <= 8) e = cudaLaunchKernelEx(&cfg, k_layer_head<8>, p);
-  else e = cudaLaunchKernelEx(&cfg, k_layer_head<16>, p);
+  const cudaLaunchConfig_t cfg = config((p.E + 7) / 8 * HEAD_SLICES + p.H / 128, HEAD_THREADS, 0, st, &attr);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_layer_head, p);
   if (e != cudaSuccess) return e;
-  return p.nc == 16 ? launch_experts<16>(maps, p, sms, st) : launch_experts<32>(maps, p, sms, st);
+  if (p.M == 1) return launch_experts<16, 1>(maps, p, sms, st);
+  if (p.M == 2) return launch_experts<16, 2>(maps, p, sms, st);
+  if (p.M <= 8) return launch_experts<16, GROUP>(maps, p, sms, st);
+  return launch_experts<32, GROUP>(maps, p, sms, st);
 }
 
 }  // namespace moe

@@ -115,11 +115,10 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
   volatile int* abort_flag = &S.abort_flag;
 
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int G = gridDim.x;
-  const int share = G - 1 - blockIdx.x;   // a share waits for later ones only, which blocks launched before it hold
+  const int G = gridDim.x, share = G - 1 - blockIdx.x;   // a share waits for later ones only, which blocks launched before it hold
   const int KU = p.KU, TT = p.TT;
-  const int64_t U = p.units;
-  const int64_t u0 = share_begin(U, G, share), u1 = share_begin(U, G, share + 1);
+  const Shares sh = p.shares;
+  const int u0 = sh.begin(share), u1 = sh.begin(share + 1), nu = u1 - u0;
   // warps that share one unit's split: a warp for a token, as a power of two
   const int mtile = min(p.M, MT);
   const int gw = mtile <= 2 ? SPLIT_WARPS / MAX_GROUPS : mtile <= 4 ? 4 : 8;
@@ -155,9 +154,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
       int st = 0;
       uint32_t ph = 0;
       bool ok = true;
-      const int64_t tile0 = u0 / KU;
-      const int ku0 = static_cast<int>(u0 - tile0 * KU), nu = static_cast<int>(u1 - u0);
-      const int rt0 = static_cast<int>(tile0 / TT), tt0 = static_cast<int>(tile0 - (int64_t)rt0 * TT);
+      const int tile0 = u0 / KU, ku0 = u0 - tile0 * KU, rt0 = tile0 / TT, tt0 = tile0 - rt0 * TT;
       auto next = [&](int& rt, int& tt, int& ku) {
         if (++ku == KU) { ku = 0; if (++tt == TT) { tt = 0; ++rt; } }
       };
@@ -201,9 +198,8 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
     int st = 0, slot = 0, seg = 0;
     uint32_t ph = 0;
     bool ok = true;
-    int ku = static_cast<int>(u0 % KU);
+    int ku = u0 % KU;
     bool first = true;
-    const int nu = static_cast<int>(u1 - u0);
     for (int i = 0; i < nu; ++i) {
       const int b = seg & 1;
       if (first && !mbar_wait(&S.acce[b], ((seg >> 1) & 1) ^ 1, deadline, abort_flag)) { fail(2); ok = false; break; }
@@ -246,9 +242,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
     const int sw = warp - WARP_SPLIT0, grp = sw / gw, ngrp = SPLIT_WARPS / gw, wi = sw % gw;
     const int kk = lane >> 4, g8 = lane & 15;
     constexpr int IP = MT / 8;                  // tokens per warp at most
-    int64_t tile = u0 / KU;
-    int ku = static_cast<int>(u0 - tile * KU), tt = static_cast<int>(tile % TT);
-    const int nu = static_cast<int>(u1 - u0);
+    int ku = u0 % KU, tt = u0 / KU % TT;
     auto advance = [&](int n) {
       ku += n;
       while (ku >= KU) { ku -= KU; if (++tt == TT) tt = 0; }
@@ -306,12 +300,12 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
     constexpr int CB = 64 / TB;             // parts per batch: 64 loads in flight
     int seg = 0;
     bool ok = true;
-    for (int64_t u = u0; u < u1 && ok; ++seg) {
-      const int64_t tile = u / KU, t0 = tile * KU, t1 = t0 + KU, ue = min(t1, u1);
-      const int rt = static_cast<int>(tile / TT), tt = static_cast<int>(tile - (int64_t)rt * TT);
+    for (int u = u0; u < u1 && ok; ++seg) {
+      const int tile = u / KU, t0 = tile * KU, t1 = t0 + KU, ue = min(t1, u1);
+      const int rt = tile / TT, tt = tile - rt * TT;
       const int m = min(MT, p.M - tt * MT), n = rt * 128 + row;
       const bool mine = u == t0;                           // this share starts the tile and so finishes it
-      const int c1 = mine ? share_of(U, G, t1 - 1) : share;   // shares after this one that hold parts of it
+      const int c1 = mine ? sh.of(t1 - 1) : share;   // shares after this one that hold parts of it
       const int b = seg & 1;
       const float bv = (p.bias && n < p.N) ? __ldg(p.bias + n) : 0.0f;
       if (!mbar_wait(&S.accf[b], (seg >> 1) & 1, deadline, abort_flag)) { fail(7); break; }

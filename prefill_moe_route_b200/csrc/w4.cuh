@@ -95,11 +95,5 @@ __device__ __forceinline__ uint32_t part_peek(const uint32_t* p) {
 }
 __device__ __forceinline__ float part_value(uint32_t word) { return __uint_as_float(~word); }
 
-// Units [lo, hi) of `total` that share c of `g` shares takes, and the share that holds unit u.
-__device__ __forceinline__ int64_t share_begin(int64_t total, int g, int c) { return total * c / g; }
-__device__ __forceinline__ int share_of(int64_t total, int g, int64_t u) {
-  return static_cast<int>(((u + 1) * g - 1) / total);
-}
-
 }  // namespace w4
 }  // namespace moe
