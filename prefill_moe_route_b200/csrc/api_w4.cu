@@ -52,7 +52,7 @@ static int linear_plan(const moe_linear_shape_t& s, int sms, LinearPlan* p) {
 }
 
 struct LayerPlan {
-  size_t o_part1, o_part2, o_dot, o_ssq, o_xop, o_xsf, o_mop, o_msf, total;
+  size_t o_part1, o_part2, o_sig, o_rstd, o_xop, o_xsf, o_mop, o_msf, total;
 };
 
 static int layer_plan(const moe_layer_shape_t& s, LayerPlan* p) {
@@ -69,8 +69,8 @@ static int layer_plan(const moe_layer_shape_t& s, LayerPlan* p) {
   const size_t KC = s.H / 128, tiles = (size_t)std::min(s.E, 16 * s.topk) * (s.I / 128) + s.shared_I / 128;
   p->o_part1 = take((size_t)kMaxGrid * 32 * 128 * 4);
   p->o_part2 = take((size_t)kMaxGrid * 16 * 128 * 4);
-  p->o_dot = take((size_t)4 * 16 * s.E * 4);
-  p->o_ssq = take(4 * 16 * 4);
+  p->o_sig = take((size_t)16 * s.E * 4);
+  p->o_rstd = take(16 * 4);
   p->o_xop = take(KC * 32 * 128);
   p->o_xsf = take(KC * 512);
   p->o_mop = take(tiles * 32 * 128);
@@ -218,8 +218,8 @@ int moe_layer_w4(const moe_layer_shape_t* shape, const moe_layer_weights_t* w, c
   p.sync = reinterpret_cast<int32_t*>(ws + 64);
   p.part1 = reinterpret_cast<uint32_t*>(ws + pl.o_part1);
   p.part2 = reinterpret_cast<uint32_t*>(ws + pl.o_part2);
-  p.dot = reinterpret_cast<float*>(ws + pl.o_dot);
-  p.ssq = reinterpret_cast<float*>(ws + pl.o_ssq);
+  p.sig = reinterpret_cast<float*>(ws + pl.o_sig);
+  p.rstd = reinterpret_cast<float*>(ws + pl.o_rstd);
   p.xop = ws + pl.o_xop; p.xsf = ws + pl.o_xsf;
   p.mop = ws + pl.o_mop; p.msf = ws + pl.o_msf;
   p.ldx = shape->ldx; p.ldo = shape->ldo;

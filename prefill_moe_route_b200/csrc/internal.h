@@ -194,7 +194,7 @@ struct LayerParams {
   int32_t* status;
   int32_t* sync;            // [0] next task, [1] quarters of mid tiles stored; k_layer_head zeroes both
   uint32_t *part1, *part2;  // parts of cut tiles: [grid][gate, up of the tokens][128], [grid][tokens][128]; zero between calls
-  float *dot, *ssq;         // slices of x . router_w [4][16][E], of sum x^2 [4][16]
+  float *sig, *rstd;        // sigmoids of the logits [M][E]; the norm's factors [M]
   uint8_t *xop, *xsf;       // the tokens' operand blocks and scale blocks [H/128]
   uint8_t *mop, *msf;       // mid's, one per GEMM1 tile
   int64_t ldx, ldo;

@@ -3,10 +3,10 @@
 // weights with bf16 activations, an always-used shared expert, the residual.
 //
 //   k_layer_head     the router's logits (bf16 MMAs, nothing rounded) and the
-//                    norm's sums of squares, cut along K; and the tokens as
+//                    norm's sums of squares, cut along K, to sigmoids; and the tokens as
 //                    tensor-core operand columns (w4.cuh) of x * norm weight.  The
 //                    norm's 1 / rms is a factor of the token, applied to the sums.
-//   k_layer_experts  one CTA an SM.  Each routes the tokens from the logits (the
+//   k_layer_experts  one CTA an SM.  Each routes the tokens from the sigmoids (the
 //                    same everywhere), then streams weights: GEMM1 over the selected
 //                    experts' gate and up rows, SwiGLU, mid as operand columns
 //                    scaled by the routing weight, and GEMM2, in which the experts
@@ -32,7 +32,7 @@ namespace layer {
 using namespace w4;
 
 constexpr int HEAD_THREADS = 256;
-constexpr int HEAD_SLICES = 4;     // CTAs along K of 8 experts' logits
+constexpr int HEAD_SLICES = 8;     // CTAs along K of 8 experts' logits
 constexpr int GROUP = 4;           // tokens whose sums one warp keeps
 constexpr int MAX_GROUPS = 4;
 // warps: 0 weights, 1 MMA, 2 operands, 3 routing only, then four a group of tokens for the sums
@@ -124,20 +124,30 @@ __device__ __forceinline__ void split_chunk(const LayerParams& p, int kc) {
   }
 }
 
-// CTAs [0, groups * HEAD_SLICES): the logits of 8 experts over a slice of K, a
-// warp every 32nd block of 32 K.  The other CTAs: one operand chunk each.
+// Clusters of HEAD_SLICES CTAs.  The first ceil(E / 8): the logits of 8 experts, a
+// slice of K a CTA, a warp every 32nd block of 32 K; the slices meet in rank 0.
+// The other clusters: one operand chunk a CTA.
 // A thread holds 8 consecutive K of token g, of token g + 8 and of expert g (g =
 // lane / 4): two MMAs' fragments with K permuted the same way on both sides.
 // The norm weight multiplies the router weight; the product of two 8-bit
 // significands is two bf16 exactly, so nothing is rounded before the sums.
-__global__ void __launch_bounds__(HEAD_THREADS, 2) k_layer_head(const LayerParams p) {
-  constexpr int BATCH = 6;   // blocks in flight
+__global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREADS, 3) k_layer_head(const LayerParams p) {
+  constexpr int BATCH = 3;   // blocks in flight
+  {  // the router's rows start for L2 while the kernel before ends
+    const int e = blockIdx.x / HEAD_SLICES * 8 + (threadIdx.x >> 2 & 7);
+    if (e < p.E && (threadIdx.x & 3) == 0)
+      for (int b = blockIdx.x % HEAD_SLICES * 8 + (threadIdx.x >> 5); b < p.H / 32; b += 8 * HEAD_SLICES)
+        prefetch_l2_line(p.router_w + (int64_t)e * p.H + b * 32);
+  }
   pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) { p.sync[0] = 0; p.sync[1] = 0; }
   pdl_launch_dependents();
   const int M = p.M, H = p.H, E = p.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nlogit = (E + 7) / 8 * HEAD_SLICES;
-  if (blockIdx.x >= nlogit) { split_chunk(p, blockIdx.x - nlogit); return; }
+  if (blockIdx.x >= nlogit) {   // a whole cluster
+    if (blockIdx.x - nlogit < H / 128) split_chunk(p, blockIdx.x - nlogit);
+    return;
+  }
   const int eg = blockIdx.x / HEAD_SLICES, slice = blockIdx.x % HEAD_SLICES;
   const int g = lane >> 2, kq = (lane & 3) * 8, nblk = H / 32;
   const bool e_ok = eg * 8 + g < E, t0 = g < M, t1 = g + 8 < M, norm = p.norm_w != nullptr;
@@ -174,107 +184,90 @@ __global__ void __launch_bounds__(HEAD_THREADS, 2) k_layer_head(const LayerParam
         }
         mma_16816(d, a[0], c[0], a[1], c[1], bl[0], bl[1]);
         mma_16816(d, a[2], c[2], a[3], c[3], bl[2], bl[3]);
-        if (eg == 0) {
-          float f[8];
-          unpack8(xa[i], f);
+        float f[8];
+        unpack8(xa[i], f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ss0 = fmaf(f[j], f[j], ss0);
-          unpack8(xb[i], f);
+        for (int j = 0; j < 8; ++j) ss0 = fmaf(f[j], f[j], ss0);
+        unpack8(xb[i], f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ss1 = fmaf(f[j], f[j], ss1);
-        }
+        for (int j = 0; j < 8; ++j) ss1 = fmaf(f[j], f[j], ss1);
       }
       mma_16816(d, a[0], c[0], a[1], c[1], bh[0], bh[1]);
       mma_16816(d, a[2], c[2], a[3], c[3], bh[2], bh[3]);
     }
   }
   __shared__ float sd[8][16][8], sq[8][16];
+  __shared__ float cs[HEAD_SLICES][16 * 8 + 16];   // rank 0's: every slice's sums
   *reinterpret_cast<float2*>(&sd[warp][g][(lane & 3) * 2]) = make_float2(d[0], d[1]);
   *reinterpret_cast<float2*>(&sd[warp][g + 8][(lane & 3) * 2]) = make_float2(d[2], d[3]);
-  if (norm && eg == 0) {
 #pragma unroll
-    for (int o = 1; o <= 2; o *= 2) {
-      ss0 += __shfl_xor_sync(0xFFFFFFFFu, ss0, o);
-      ss1 += __shfl_xor_sync(0xFFFFFFFFu, ss1, o);
-    }
-    if ((lane & 3) == 0) { sq[warp][g] = ss0; sq[warp][g + 8] = ss1; }
+  for (int o = 1; o <= 2; o *= 2) {
+    ss0 += __shfl_xor_sync(0xFFFFFFFFu, ss0, o);
+    ss1 += __shfl_xor_sync(0xFFFFFFFFu, ss1, o);
   }
+  if ((lane & 3) == 0) { sq[warp][g] = ss0; sq[warp][g + 8] = ss1; }
   __syncthreads();
-  if (threadIdx.x < 128) {
-    const int t = threadIdx.x >> 3, e = eg * 8 + (threadIdx.x & 7);
+  if (threadIdx.x < 128 + 16) {
+    const int i = threadIdx.x;
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += sd[i][t][threadIdx.x & 7];
-    if (t < M && e < E) p.dot[((int64_t)slice * MAX_M + t) * E + e] = sum;
-  } else if (norm && eg == 0 && threadIdx.x < 128 + 16) {
-    const int t = threadIdx.x - 128;
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += sq[i][t];
-    p.ssq[slice * MAX_M + t] = sum;
+    for (int q = 0; q < 8; ++q) sum += i < 128 ? sd[q][i >> 3][i & 7] : sq[q][i - 128];
+    st_shared_cluster_f32(mapa_shared(smem_u32(&cs[slice][i]), 0), sum);
   }
+  cluster_arrive_release();
+  cluster_wait_acquire();   // rank 0's shared memory outlives the stores: it leaves last
+  if (slice != 0 || threadIdx.x >= 128) return;
+  const int t = threadIdx.x >> 3, e = eg * 8 + (threadIdx.x & 7);
+  if (t >= M) return;
+  float dot = 0.0f, sum = 0.0f, rstd = 1.0f;
+#pragma unroll
+  for (int q = 0; q < HEAD_SLICES; ++q) { dot += cs[q][threadIdx.x]; sum += cs[q][128 + t]; }
+  if (norm) rstd = 1.0f / sqrtf(sum / (float)H + p.eps);
+  if (e < E) p.sig[t * E + e] = sigmoid_spec(dot * rstd);
+  if (eg == 0 && (threadIdx.x & 7) == 0) p.rstd[t] = rstd;
 }
 
-// Routes token t with one warp from its logits' slices: sigmoid, the top k of
-// sigmoid + bias in k rounds (a tie going to the lower expert), weights as in
-// route_token_warp.  Returns the norm's factor of the token.  Every CTA runs
-// this once, cold, so the code is kept short (the sigmoids in a loop through
-// `scratch`, 64 KPER words of the warp's own).
+// Routes token t with one warp from its experts' sigmoids: the top k of sigmoid
+// + bias in k rounds (a tie going to the lower expert), weights as in
+// route_token_warp.  Every CTA runs this once, cold, so the code is kept short.
 template <int KPER>
-__device__ __forceinline__ float pick(const LayerParams& p, int t, int* ids, float* wts, uint32_t* mask,
-                                      uint32_t* scratch) {
+__device__ __forceinline__ void pick(const LayerParams& p, int t, int* ids, float* wts, uint32_t* mask, float* ssig) {
   const int lane = threadIdx.x & 31, E = p.E, k = p.topk;
-  uint32_t* skey = scratch;                                     // [KPER][32] bias, then selection keys
-  float* ssig = reinterpret_cast<float*>(scratch + 32 * KPER);  // [KPER][32] x . router_w, then sigmoids
-  float rstd = 1.0f;
+  uint32_t key[KPER];
   {
-    float part[HEAD_SLICES][KPER], ssq = 0.0f;
+    float sg[KPER], bias[KPER];
 #pragma unroll
     for (int i = 0; i < KPER; ++i) {
       const int e = lane + 32 * i;
-#pragma unroll
-      for (int q = 0; q < HEAD_SLICES; ++q) part[q][i] = e < E ? __ldcg(p.dot + (q * MAX_M + t) * E + e) : 0.0f;
-      skey[i * 32 + lane] = p.bias && e < E ? __float_as_uint(__ldg(p.bias + e)) : 0u;
-    }
-    if (p.norm_w) {
-#pragma unroll
-      for (int q = 0; q < HEAD_SLICES; ++q) ssq += __ldcg(p.ssq + q * MAX_M + t);
-      rstd = 1.0f / sqrtf(ssq / (float)p.H + p.eps);
+      sg[i] = e < E ? __ldcg(p.sig + t * E + e) : 0.0f;
+      bias[i] = p.bias && e < E ? __ldg(p.bias + e) : 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < KPER; ++i) {
-      float l = part[0][i];
-#pragma unroll
-      for (int q = 1; q < HEAD_SLICES; ++q) l += part[q][i];
-      ssig[i * 32 + lane] = l;
+      ssig[lane + 32 * i] = sg[i];
+      key[i] = lane + 32 * i < E ? float_order_key(p.bias ? __fadd_rn(sg[i], bias[i]) : sg[i]) : 0u;
     }
   }
-#pragma unroll 1
-  for (int i = 0; i < KPER; ++i) {
-    const float sg = sigmoid_spec(ssig[i * 32 + lane] * rstd);
-    ssig[i * 32 + lane] = sg;
-    const float sc = p.bias ? __fadd_rn(sg, __uint_as_float(skey[i * 32 + lane])) : sg;
-    skey[i * 32 + lane] = lane + 32 * i < E ? float_order_key(sc) : 0u;
-  }
   __syncwarp();
-  uint32_t key[KPER];
-#pragma unroll
-  for (int i = 0; i < KPER; ++i) key[i] = skey[i * 32 + lane];
   float denom = 0.0f, mine = 0.0f;
   int id = 0;
 #pragma unroll 1
   for (int j = 0; j < k; ++j) {
-    uint32_t best = key[0];
-    int bi = 0;
+    uint32_t b[KPER];   // tournament: the lower of equal keys' experts is on the left
+    int x[KPER];
 #pragma unroll
-    for (int i = 1; i < KPER; ++i)
-      if (key[i] > best) { best = key[i]; bi = i; }
-    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-    const int e = (int)__reduce_min_sync(0xFFFFFFFFu, best == top ? (uint32_t)(lane + 32 * bi) : 0xFFFFFFFFu);
-    const float s = ssig[e];
+    for (int i = 0; i < KPER; ++i) { b[i] = key[i]; x[i] = i; }
+#pragma unroll
+    for (int w = 1; w < KPER; w *= 2)
+#pragma unroll
+      for (int i = 0; i < KPER; i += 2 * w)
+        if (b[i + w] > b[i]) { b[i] = b[i + w]; x[i] = x[i + w]; }
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, b[0]);
+    const int e = (int)__reduce_min_sync(0xFFFFFFFFu, b[0] == top ? (uint32_t)(lane + 32 * x[0]) : 0xFFFFFFFFu);
 #pragma unroll
     for (int i = 0; i < KPER; ++i)
       if (lane + 32 * i == e) key[i] = 0u;   // taken (below every key of a number or a NaN)
+    const float s = ssig[e];
     denom = __fadd_rn(denom, s);
     if (lane == j) { id = e; mine = s; }
   }
@@ -283,7 +276,6 @@ __device__ __forceinline__ float pick(const LayerParams& p, int t, int* ids, flo
     wts[lane] = __fmul_rn(__fdiv_rn(mine, denom), p.scale);
     atomicOr(mask + (id >> 5), 1u << (id & 31));
   }
-  return rstd;
 }
 
 // NC: operand columns; TG: tokens a warp's group holds (1 and 2 for as many
@@ -328,10 +320,10 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
   int ticket = 0;
   if (threadIdx.x == 0) ticket = atomicAdd(p.sync, 1);   // in flight while routing runs
   if (warp < M) {   // one token a warp: there are at least M warps
-    uint32_t* scratch = reinterpret_cast<uint32_t*>(abuf) + warp * 2 * kMaxE;   // in the idle ring
-    const float r = E <= 256 ? pick<8>(p, warp, S.ids + warp * topk, S.wts + warp * topk, S.mask, scratch)
-                             : pick<kMaxE / 32>(p, warp, S.ids + warp * topk, S.wts + warp * topk, S.mask, scratch);
-    if (lane == 0) S.rstd[warp] = r;
+    float* scratch = reinterpret_cast<float*>(abuf) + warp * kMaxE;   // in the idle ring
+    if (E <= 256) pick<8>(p, warp, S.ids + warp * topk, S.wts + warp * topk, S.mask, scratch);
+    else pick<kMaxE / 32>(p, warp, S.ids + warp * topk, S.wts + warp * topk, S.mask, scratch);
+    if (lane == 0) S.rstd[warp] = __ldcg(p.rstd + warp);
     fence_proxy_async_smem();   // the ring's next writers are asynchronous copies
   }
   __syncthreads();
@@ -546,37 +538,44 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     // Adds the later shares' parts [share + 1, c1] of NV values per row, in K
     // order, to v; value i is token t0 + i % TG's.
     auto live = [&](int i) { return t0 + (i & (TG - 1)) < M; };
-    auto gather = [&](uint32_t* part, int share, int c1, auto& v, auto nv_const) -> bool {
-      constexpr int NV = decltype(nv_const)::value, CB = NV >= 2 ? 32 / NV : 16;   // parts per batch
+    auto peek = [&](const uint32_t* part, int cb, int c1, auto& w) {   // parts cb .. c1, as many as w holds
+      constexpr int CB = std::extent_v<std::remove_reference_t<decltype(w)>, 0>;
+      constexpr int NV = std::extent_v<std::remove_reference_t<decltype(w)>, 1>;
+#pragma unroll
+      for (int c = 0; c < CB; ++c)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          w[c][i] = live(i) && cb + c <= c1 ? part_peek(part + (cb + c) * (MAX_GROUPS * NV * 128) + i * 128) : 1u;
+    };
+    auto gather = [&](uint32_t* part, int share, int c1, auto& v, auto& w) -> bool {   // w: the first batch, peeked
+      constexpr int CB = std::extent_v<std::remove_reference_t<decltype(w)>, 0>;
+      constexpr int NV = std::extent_v<std::remove_reference_t<decltype(w)>, 1>;
+      uint32_t spins = 0;
 #pragma unroll 1
-      for (int cb = share + 1; cb <= c1; cb += CB) {
-        uint32_t w[CB][NV];
-        uint32_t spins = 0;
-        for (;;) {
-          bool all = true;
+      for (int cb = share + 1; cb <= c1;) {
+        bool all = true;
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+#pragma unroll
+          for (int i = 0; i < NV; ++i) all &= w[c][i] != 0u;
+        if (all) {
 #pragma unroll
           for (int c = 0; c < CB; ++c) {
-            const uint32_t* src = part + min(cb + c, c1) * (MAX_GROUPS * NV * 128);
+            if (cb + c > c1) break;
+            uint32_t* src = part + (cb + c) * (MAX_GROUPS * NV * 128);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) w[c][i] = live(i) && cb + c <= c1 ? part_peek(src + i * 128) : 1u;
+            for (int i = 0; i < NV; ++i) {
+              v[i] += part_value(w[c][i]);
+              if (live(i)) __stcg(src + i * 128, 0u);   // empty again for the next call
+            }
           }
-#pragma unroll
-          for (int c = 0; c < CB; ++c)
-#pragma unroll
-            for (int i = 0; i < NV; ++i) all &= w[c][i] != 0u;
-          if (all) break;
-          if ((++spins & 15u) == 0 && (*abort_flag || globaltimer() > deadline)) { fail(8); return false; }
+          cb += CB;
+          if (cb > c1) break;
+        } else if ((++spins & 15u) == 0 && (*abort_flag || globaltimer() > deadline)) {
+          fail(8);
+          return false;
         }
-#pragma unroll
-        for (int c = 0; c < CB; ++c) {
-          if (cb + c > c1) break;
-          uint32_t* src = part + (cb + c) * (MAX_GROUPS * NV * 128);
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            v[i] += part_value(w[c][i]);
-            if (live(i)) __stcg(src + i * 128, 0u);   // empty again for the next call
-          }
-        }
+        peek(part, cb, c1, w);
       }
       return true;
     };
@@ -589,6 +588,10 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
         const bool mine = u == tb;   // this share starts the tile and so finishes it
         const int c1 = mine ? (k.gemm == 1 ? sh1 : sh2).of(te - 1) : k.share;
         const int b = seg & 1;
+        // most parts are there before this share's own sum is: look for them first
+        uint32_t w1[16 / TG][2 * TG], w2[16 / TG][TG];
+        if (k.gemm == 1) peek(part1, k.share + 1, c1, w1);
+        else peek(part2, k.share + 1, c1, w2);
         if (!mbar_wait(&S.accf[b], (seg >> 1) & 1, deadline, abort_flag)) { fail(9); ok = false; break; }
         __syncwarp();
         tc_fence_after();
@@ -627,7 +630,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
                 for (int t = 0; t < TG; ++t)
                   if (live(t) && S.ids[(t0 + t) * topk + j] == w.e) wt[t] = S.wts[(t0 + t) * topk + j];
             }
-            if (!gather(part1, k.share, c1, v, std::integral_constant<int, 2 * TG>())) { ok = false; break; }
+            if (!gather(part1, k.share, c1, v, w1)) { ok = false; break; }
             float m[TG];
             int s[TG];
 #pragma unroll
@@ -658,9 +661,8 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
                   }
                 }
             }
-            __threadfence();
-            __syncwarp();
-            if (lane == 0 && !(p.test_withhold && tile == 0)) atomicAdd(p.sync + 1, 1);
+            __syncwarp();   // the release below covers the warp's stores
+            if (lane == 0 && !(p.test_withhold && tile == 0)) red_release_gpu(p.sync + 1, 1);
           }
         } else {
           if (!mine) {
@@ -674,7 +676,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
 #pragma unroll
             for (int t = 0; t < TG; ++t)
               r[t] = p.residual && live(t) ? __uint_as_float((uint32_t)__ldg(p.x + (t0 + t) * p.ldx + h) << 16) : 0.0f;
-            if (!gather(part2, k.share, c1, v, std::integral_constant<int, TG>())) { ok = false; break; }
+            if (!gather(part2, k.share, c1, v, w2)) { ok = false; break; }
 #pragma unroll
             for (int t = 0; t < TG; ++t)
               if (live(t)) p.out[(t0 + t) * p.ldo + h] = bf16_bits(v[t] + r[t]);
@@ -728,7 +730,8 @@ static cudaError_t launch_experts(const CUtensorMap* m, const LayerParams& p, in
 cudaError_t launch_layer_w4(const CUtensorMap* maps, const LayerParams& p, int sms, cudaStream_t st) {
   using namespace layer;
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = config((p.E + 7) / 8 * HEAD_SLICES + p.H / 128, HEAD_THREADS, 0, st, &attr);
+  const int chunks = (p.H / 128 + HEAD_SLICES - 1) / HEAD_SLICES * HEAD_SLICES;   // whole clusters
+  const cudaLaunchConfig_t cfg = config((p.E + 7) / 8 * HEAD_SLICES + chunks, HEAD_THREADS, 0, st, &attr);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, k_layer_head, p);
   if (e != cudaSuccess) return e;
   if (p.M == 1) return launch_experts<16, 1>(maps, p, sms, st);

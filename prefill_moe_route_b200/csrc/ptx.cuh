@@ -132,7 +132,14 @@ __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t cluster_saddr) {
   return v;
 }
 
+__device__ __forceinline__ void st_shared_cluster_f32(uint32_t cluster_saddr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_saddr), "f"(v) : "memory");
+}
+
 // ------------------------------------------------------------ global flags
+__device__ __forceinline__ void red_release_gpu(int32_t* p, int32_t v) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
 __device__ __forceinline__ void st_release_gpu(int32_t* p, int32_t v) {
   asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
