@@ -43,7 +43,7 @@ static int linear_plan(const moe_linear_shape_t& s, int sms, LinearPlan* p) {
   // the parts come first and in one place for every shape: they are zero
   // between calls, the operand blocks behind them are not
   p->o_xop = p->total = kLinearHeader + (size_t)kMaxGrid * p->mt * 128 * 4;
-  if (p->nc >= 64) {
+  if (p->nc >= 32) {   // made by a kernel of its own
     p->o_xop = p->total = kLinearHeader + (size_t)kMaxGrid * 64 * 128 * 4;
     p->o_xsf = p->o_xop + (size_t)p->TT * p->KC * p->nc * 128;
     p->total = p->o_xsf + (size_t)p->TT * p->KC * 512;

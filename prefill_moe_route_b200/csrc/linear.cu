@@ -1,5 +1,5 @@
 // linear.cu -- y = x W^T (+ bias) for few tokens: MXFP4 weights, bf16
-// activations, fp32 sums, one launch.
+// activations, fp32 sums, one launch (two above 8 tokens).
 //
 // Bound: the weights' bytes.  The product runs on the tensor cores with the
 // weights on the MMA's M side straight from their packed 4-bit form (no
@@ -10,9 +10,10 @@
 // others' parts in K order (so results do not depend on timing); those are the
 // first thing that their CTAs finish, and the starting share's last.
 //
-// Roles: one thread streams tiles (TMA) and their scale blocks (bulk copy),
-// eight warps split the tokens' K chunks into the operand ring, one thread
-// issues the MMAs, four warps read the sums out of TMEM.
+// Roles: one thread streams tiles (TMA) and their scale blocks (bulk copy), a
+// warp for each token splits its K chunks into the operand ring (above 8 tokens
+// k_split_x does it before, and the stream brings them), one thread issues the
+// MMAs, four warps for each 16 tokens read the sums out of TMEM.
 #include <atomic>
 
 #include "w4.cuh"
@@ -22,28 +23,29 @@ namespace linear {
 
 using namespace w4;
 
-constexpr int SPLIT_WARPS = 8;
-constexpr int MAX_GROUPS = 4;       // units whose operand is being split at once
 constexpr int WARP_SPLIT0 = 2;
 constexpr int UK = 2;               // K chunks of 128 in a unit
 constexpr int SF_SLOTS = 4;         // TMEM scale slots: per chunk 4 columns of weight scales + 4 of token scales
 
-template <int NC>
-struct Cfg {                        // NC: operand columns, two per token
+// NC: operand columns, two per token.  SW: warps that split the tokens' K chunks
+// in the kernel; 0: k_split_x has done it before.  Measured (us, N = K = 6144, 8
+// split warps / 16 / before): 4 tokens 7.7 / 8.1 / 9.4, 8 tokens 9.1 / 8.3 / 9.6,
+// 16 tokens 11.5 / 10.9 / 10.6 (N = 12288: 17.4 / 15.8 / 13.5).
+template <int NC, int SW>
+struct Cfg {
   static constexpr int MT = NC / 2;
-  // Above 16 tokens every CTA splitting its own K chunks costs more than one
-  // small kernel that does it once (k_split_x) and a bulk copy per unit.
-  static constexpr bool PRE = NC >= 64;
-  static constexpr int WARP_EPI0 = WARP_SPLIT0 + (PRE ? 2 : SPLIT_WARPS);   // the two are idle: TMEM quarters
-  static constexpr int THREADS = (WARP_EPI0 + 4) * 32;
+  static constexpr bool PRE = SW == 0;
+  static constexpr int WARP_EPI0 = WARP_SPLIT0 + (PRE ? 2 : SW);   // the two are idle: TMEM quarters
+  // the sums of 16 tokens a group of four warps: one after another their trips
+  // through L2 would add up
+  static constexpr int EG = MT > 16 ? MT / 16 : 1, ET = MT / EG;
+  static constexpr int THREADS = (WARP_EPI0 + 4 * EG) * 32;
   static constexpr int B_TILE = NC * 128;
   static constexpr int A_BYTES = UK * A_TILE, B_BYTES = UK * B_TILE, SF_BYTES = UK * SF_BLOCK;
   static constexpr int STAGE = A_BYTES + B_BYTES + 2 * SF_BYTES;   // weights, tokens, their scales
   static constexpr int STAGES = NC >= 128 ? 3 : NC >= 64 ? 4 : 5;
   static constexpr int TMEM_COLS = NC >= 128 ? 512 : 256;
   static constexpr int SF_COL0 = 2 * NC;
-  // a group of split warps two rounds ahead of the MMA would read a slot's old phase
-  static_assert(PRE || MAX_GROUPS <= STAGES, "ring depth");
 };
 
 struct Smem {
@@ -52,58 +54,38 @@ struct Smem {
   int abort_flag;
 };
 
-template <int NC>
+template <int NC, int SW>
 constexpr int smem_bytes() {
-  return Cfg<NC>::STAGES * Cfg<NC>::STAGE + (int)sizeof(Smem) + 1024;
+  static_assert(Cfg<NC, SW>::STAGES * Cfg<NC, SW>::STAGE + sizeof(Smem) + 1024 <= 232448, "shared memory");
+  return Cfg<NC, SW>::STAGES * Cfg<NC, SW>::STAGE + (int)sizeof(Smem) + 1024;
 }
-static_assert(smem_bytes<16>() <= 232448 && smem_bytes<32>() <= 232448 && smem_bytes<64>() <= 232448 &&
-                  smem_bytes<128>() <= 232448, "shared memory");
 
-// 8 values of JB tokens' K chunk each: 8 bf16 in, 8 bytes of both operand
-// columns out; four neighbouring lanes hold a block of 32.  The JB chains run
-// side by side: one alone is a few hundred clocks of dependent conversions.
-template <int JB>
-__device__ __forceinline__ void split_items(const uint4* u, uint8_t* tile, uint8_t* sf, int n0, int step, int mt, int g8) {
-  uint32_t w[JB][4], am[JB];
+// 8 values of a token's K chunk: 8 bf16 in, 8 bytes of both operand columns (n, n
+// + mt) out; four neighbouring lanes hold a block of 32.
+__device__ __forceinline__ void split_item(const uint4& u, uint8_t* tile, uint8_t* sf, int n, int mt, int g8) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t am = 0;   // largest magnitudes as bf16 bits
 #pragma unroll
-  for (int j = 0; j < JB; ++j) {
-    w[j][0] = u[j].x; w[j][1] = u[j].y; w[j][2] = u[j].z; w[j][3] = u[j].w;
-    uint32_t a = 0;   // largest magnitudes as bf16 bits
+  for (int i = 0; i < 4; ++i) am = max_u16x2(am, w[i] & 0x7FFF7FFFu);
+  am = max(am & 0xFFFFu, am >> 16);
+  am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+  am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+  const int s = split_exp(__uint_as_float(am << 16));
+  uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a = max_u16x2(a, w[j][i] & 0x7FFF7FFFu);
-    am[j] = max(a & 0xFFFFu, a >> 16);
-  }
-#pragma unroll
-  for (int j = 0; j < JB; ++j) am[j] = max(am[j], __shfl_xor_sync(0xFFFFFFFFu, am[j], 1));
-#pragma unroll
-  for (int j = 0; j < JB; ++j) am[j] = max(am[j], __shfl_xor_sync(0xFFFFFFFFu, am[j], 2));
-  uint32_t hi[JB][4], lo[JB][4];
-  int s[JB];
-#pragma unroll
-  for (int j = 0; j < JB; ++j) {
-    s[j] = split_exp(__uint_as_float(am[j] << 16));
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      split_f16x2(s[j] == SPLIT_NAN ? 0x7E007E00u : f16x2_scaled(w[j][i], s[j]), hi[j][i], lo[j][i]);
-  }
-#pragma unroll
-  for (int j = 0; j < JB; ++j) {
-    const int n = n0 + j * step;
-    *reinterpret_cast<uint2*>(tile + tile_byte(n, g8 * 8)) =
-        make_uint2(hi[j][0] | hi[j][1] << 16, hi[j][2] | hi[j][3] << 16);
-    *reinterpret_cast<uint2*>(tile + tile_byte(mt + n, g8 * 8)) =
-        make_uint2(lo[j][0] | lo[j][1] << 16, lo[j][2] | lo[j][3] << 16);
-    if ((g8 & 3) == 0) {
-      sf[sf_byte(n, g8 >> 2)] = static_cast<uint8_t>(split_code_hi(s[j]));
-      sf[sf_byte(mt + n, g8 >> 2)] = static_cast<uint8_t>(split_code_lo(s[j]));
-    }
+  for (int i = 0; i < 4; ++i) split_f16x2(s == SPLIT_NAN ? 0x7E007E00u : f16x2_scaled(w[i], s), hi[i], lo[i]);
+  *reinterpret_cast<uint2*>(tile + tile_byte(n, g8 * 8)) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+  *reinterpret_cast<uint2*>(tile + tile_byte(mt + n, g8 * 8)) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+  if ((g8 & 3) == 0) {
+    sf[sf_byte(n, g8 >> 2)] = static_cast<uint8_t>(split_code_hi(s));
+    sf[sf_byte(mt + n, g8 >> 2)] = static_cast<uint8_t>(split_code_lo(s));
   }
 }
 
-template <int NC>
-__global__ void __launch_bounds__(Cfg<NC>::THREADS, 1)
+template <int NC, int SW>
+__global__ void __launch_bounds__(Cfg<NC, SW>::THREADS, 1)
 k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
-  using C = Cfg<NC>;
+  using C = Cfg<NC, SW>;
   constexpr int MT = C::MT, WARP_EPI0 = C::WARP_EPI0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -119,13 +101,15 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
   const int KU = p.KU, TT = p.TT;
   const Shares sh = p.shares;
   const int u0 = sh.begin(share), u1 = sh.begin(share + 1), nu = u1 - u0;
-  // warps that share one unit's split: a warp for a token, as a power of two
-  const int mtile = min(p.M, MT);
-  const int gw = mtile <= 2 ? SPLIT_WARPS / MAX_GROUPS : mtile <= 4 ? 4 : 8;
+  // warps that share one unit's split, one for a token; the groups of them, two or
+  // four, must not outnumber the stages (one two rounds ahead of the MMA would
+  // read a slot's old phase)
+  const int gw = p.M <= 2 ? 2 : p.M <= 4 ? 4 : 8;
+  static_assert(C::PRE || (SW <= 8 ? SW / 2 : SW / 8) <= C::STAGES, "ring depth");
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) { mbar_init(&S.full[s], C::PRE ? 1 : 1 + gw); mbar_init(&S.empty[s], 1); }
-    for (int b = 0; b < 2; ++b) { mbar_init(&S.accf[b], 1); mbar_init(&S.acce[b], 4); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&S.accf[b], 1); mbar_init(&S.acce[b], 4 * C::EG); }
     S.abort_flag = 0;
     fence_mbar_init();
   }
@@ -238,36 +222,21 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
   } else if (warp < WARP_EPI0) {
     if constexpr (!C::PRE) {
     // ------------------------------------------------ token operand
-    // A lane owns 8 of the unit's 256 K; warp wi of the unit's gw takes tokens wi, wi + gw, ...
-    const int sw = warp - WARP_SPLIT0, grp = sw / gw, ngrp = SPLIT_WARPS / gw, wi = sw % gw;
+    // A lane owns 8 of the unit's 256 K, a warp of the unit's gw one token (all fit one token tile).
+    const int sw = warp - WARP_SPLIT0, grp = sw / gw, ngrp = SW / gw, t = sw % gw;
     const int kk = lane >> 4, g8 = lane & 15;
-    constexpr int IP = MT / 8;                  // tokens per warp at most
-    int ku = u0 % KU, tt = u0 / KU % TT;
-    auto advance = [&](int n) {
-      ku += n;
-      while (ku >= KU) { ku -= KU; if (++tt == TT) tt = 0; }
-    };
-    auto load = [&](uint4 (&v)[IP]) {
+    constexpr int PD = 4;   // units' loads in flight: a unit is consumed faster than L2 answers
+    int ku = (u0 + grp) % KU;
+    auto load = [&]() -> uint4 {   // and on to this group's next unit
       const int k = ku * (UK * 128) + lane * 8;
-#pragma unroll
-      for (int i = 0; i < IP; ++i) {
-        const int tl = i * gw + wi, t = tt * MT + tl;
-        v[i] = (tl < MT && t < p.M && k < p.K) ? __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.ldx + k))
-                                               : make_uint4(0u, 0u, 0u, 0u);
-      }
+      ku += ngrp;
+      while (ku >= KU) ku -= KU;
+      return t < p.M && k < p.K ? __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.ldx + k))
+                                : make_uint4(0u, 0u, 0u, 0u);
     };
-    // PD units' loads in flight: a unit is consumed faster than L2 answers
-    constexpr int PD = IP <= 2 ? 4 : IP <= 4 ? 2 : 1;
-    constexpr int JB = IP < 4 ? IP : 4;
-    uint4 buf[PD][IP];
-    advance(grp);
-    int ahead = grp;   // unit whose loads go out next
+    uint4 buf[PD];
 #pragma unroll
-    for (int d = 0; d < PD; ++d) {
-      if (ahead < nu) load(buf[d]);
-      advance(ngrp);
-      ahead += ngrp;
-    }
+    for (int d = 0; d < PD; ++d) buf[d] = load();
     bool ok = true;
     for (int i0 = grp; i0 < nu && ok; i0 += PD * ngrp) {
 #pragma unroll
@@ -277,17 +246,11 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
         const int st = i % C::STAGES;
         if (!mbar_wait(&S.empty[st], ((i / C::STAGES) & 1) ^ 1, deadline, abort_flag)) { fail(5); ok = false; break; }
         __syncwarp();
-        uint8_t* tb = bbuf + st * C::B_BYTES + kk * C::B_TILE;
-        uint8_t* sf = bsf + st * C::SF_BYTES + kk * SF_BLOCK;
-#pragma unroll
-        for (int j = 0; j < IP; j += JB)
-          if (j * gw + wi < mtile) split_items<JB>(buf[d] + j, tb, sf, j * gw + wi, gw, MT, g8);   // warp-uniform
+        split_item(buf[d], bbuf + st * C::B_BYTES + kk * C::B_TILE, bsf + st * C::SF_BYTES + kk * SF_BLOCK, t, MT, g8);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.full[st]);
-        if (ahead < nu) load(buf[d]);
-        advance(ngrp);
-        ahead += ngrp;
+        buf[d] = load();
       }
     }
     }
@@ -296,34 +259,40 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
     // ------------------------------------------------ sums
     const int q = warp & 3, row = 32 * q + lane;   // TMEM lane quarter = warp % 4
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    constexpr int TB = MT < 16 ? MT : 16;   // tokens per TMEM read
-    constexpr int CB = 64 / TB;             // parts per batch: 64 loads in flight
+    constexpr int TB = 8;                   // tokens per step
+    constexpr int CB = 4;                   // parts per batch: 32 loads in flight
+    const int g0 = (warp - WARP_EPI0) / 4 * C::ET;   // this group's tokens of the tile
     int seg = 0;
     bool ok = true;
     for (int u = u0; u < u1 && ok; ++seg) {
       const int tile = u / KU, t0 = tile * KU, t1 = t0 + KU, ue = min(t1, u1);
       const int rt = tile / TT, tt = tile - rt * TT;
-      const int m = min(MT, p.M - tt * MT), n = rt * 128 + row;
+      const int m = min(min(MT, p.M - tt * MT), g0 + C::ET), n = rt * 128 + row;
       const bool mine = u == t0;                           // this share starts the tile and so finishes it
       const int c1 = mine ? sh.of(t1 - 1) : share;   // shares after this one that hold parts of it
       const int b = seg & 1;
       const float bv = (p.bias && n < p.N) ? __ldg(p.bias + n) : 0.0f;
+      // parts cb .. of tokens tb .. tb + TB - 1
+      uint32_t w[CB][TB];
+      auto peek = [&](int cb, int tb) {
+#pragma unroll
+        for (int i = 0; i < CB; ++i) {
+          const uint32_t* src = p.part + ((int64_t)(cb + i) * MT + tb) * 128 + row;
+#pragma unroll
+          for (int t = 0; t < TB; ++t) w[i][t] = cb + i <= c1 && tb + t < m ? part_peek(src + t * 128) : 1u;
+        }
+      };
+      if (g0 < m) peek(share + 1, g0);   // most are there before this share's own sum is
       if (!mbar_wait(&S.accf[b], (seg >> 1) & 1, deadline, abort_flag)) { fail(7); break; }
       __syncwarp();
       tc_fence_after();
 #pragma unroll 1
-      for (int tb = 0; tb < m && ok; tb += TB) {
+      for (int tb = g0; tb < m && ok; tb += TB) {
         float v[TB];
-        if constexpr (NC == 16) {
-          float a[16];
-          tmem_ld16(tl + b * NC, a);
-          tmem_ld_wait();
-#pragma unroll
-          for (int t = 0; t < TB; ++t) v[t] = a[t] + a[MT + t];
-        } else {
-          float a[16], c[16];
-          tmem_ld16(tl + b * NC + tb, a);
-          tmem_ld16(tl + b * NC + MT + tb, c);
+        {
+          float a[8], c[8];
+          tmem_ld(tl + b * NC + tb, a);
+          tmem_ld(tl + b * NC + MT + tb, c);
           tmem_ld_wait();
 #pragma unroll
           for (int t = 0; t < TB; ++t) v[t] = a[t] + c[t];
@@ -335,37 +304,35 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
             if (tb + t < m && !(p.test_withhold && share == G - 1)) part_put(dst + t * 128, v[t]);
           continue;
         }
+        uint32_t spins = 0;
 #pragma unroll 1
-        for (int cb = share + 1; cb <= c1 && ok; cb += CB) {   // the later shares' parts, in K order
-          uint32_t w[CB][TB];
-          uint32_t spins = 0;
-          for (;;) {
-            bool all = true;
+        for (int cb = share + 1; cb <= c1;) {   // the later shares' parts, in K order
+          bool all = true;
+#pragma unroll
+          for (int i = 0; i < CB; ++i)
+#pragma unroll
+            for (int t = 0; t < TB; ++t) all &= w[i][t] != 0u;
+          if (all) {
 #pragma unroll
             for (int i = 0; i < CB; ++i) {
-              const uint32_t* src = p.part + ((int64_t)min(cb + i, c1) * MT + tb) * 128 + row;
+              if (cb + i > c1) break;
+              uint32_t* src = p.part + ((int64_t)(cb + i) * MT + tb) * 128 + row;
 #pragma unroll
-              for (int t = 0; t < TB; ++t) w[i][t] = tb + t < m ? part_peek(src + t * 128) : 1u;
+              for (int t = 0; t < TB; ++t) {
+                v[t] += part_value(w[i][t]);
+                if (tb + t < m) __stcg(src + t * 128, 0u);   // empty again for the next call
+              }
             }
-#pragma unroll
-            for (int i = 0; i < CB; ++i)
-#pragma unroll
-              for (int t = 0; t < TB; ++t) all &= w[i][t] != 0u;
-            if (all) break;
-            if ((++spins & 15u) == 0 && (*abort_flag || globaltimer() > deadline)) { fail(8); ok = false; break; }
+            cb += CB;
+            if (cb > c1) break;
+          } else if ((++spins & 15u) == 0 && (*abort_flag || globaltimer() > deadline)) {
+            fail(8);
+            ok = false;
+            break;
           }
-          if (!ok) break;
-#pragma unroll
-          for (int i = 0; i < CB; ++i) {
-            if (cb + i > c1) break;
-            uint32_t* src = p.part + ((int64_t)(cb + i) * MT + tb) * 128 + row;
-#pragma unroll
-            for (int t = 0; t < TB; ++t) {
-              v[t] += part_value(w[i][t]);
-              if (tb + t < m) __stcg(src + t * 128, 0u);   // empty again for the next call
-            }
-          }
+          peek(cb, tb);
         }
+        if (tb + TB < m) peek(share + 1, tb + TB);
         if (n < p.N && ok) {
 #pragma unroll
           for (int t = 0; t < TB; ++t) {
@@ -424,17 +391,17 @@ __global__ void __launch_bounds__(256) k_split_x(const LinearParams p) {
   const uint4 v = (t < p.M && k < p.K) ? __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.ldx + k))
                                        : make_uint4(0u, 0u, 0u, 0u);
   const int64_t blk = (int64_t)(t / MT) * p.KC + kc;
-  if (t / MT < p.TT) split_items<1>(&v, p.xop + blk * (NC * 128), p.xsf + blk * SF_BLOCK, t % MT, 0, MT, g8);
+  if (t / MT < p.TT) split_item(v, p.xop + blk * (NC * 128), p.xsf + blk * SF_BLOCK, t % MT, MT, g8);
 }
 
-template <int NC>
+template <int NC, int SW>
 static cudaError_t launch(const CUtensorMap& w, const LinearParams& p, int grid, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};   // devices on which the kernel may take its shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
-    e = cudaFuncSetAttribute(k_linear_w4<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NC>());
+    e = cudaFuncSetAttribute(k_linear_w4<NC, SW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NC, SW>());
     if (e != cudaSuccess) return e;
     if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
@@ -442,31 +409,31 @@ static cudaError_t launch(const CUtensorMap& w, const LinearParams& p, int grid,
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(Cfg<NC>::THREADS);
-  cfg.dynamicSmemBytes = smem_bytes<NC>();
+  cfg.blockDim = dim3(Cfg<NC, SW>::THREADS);
+  cfg.dynamicSmemBytes = smem_bytes<NC, SW>();
   cfg.stream = st;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if constexpr (Cfg<NC>::PRE) {
+  if constexpr (Cfg<NC, SW>::PRE) {
     cudaLaunchConfig_t pre = cfg;
     pre.gridDim = dim3(p.KC, (p.M + 15) / 16);
     pre.blockDim = dim3(256);
     pre.dynamicSmemBytes = 0;
     if ((e = cudaLaunchKernelEx(&pre, k_split_x<NC>, p)) != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, k_linear_w4<NC>, w, p);
+  return cudaLaunchKernelEx(&cfg, k_linear_w4<NC, SW>, w, p);
 }
 
 }  // namespace linear
 
 cudaError_t launch_linear_w4(const CUtensorMap& w, const LinearParams& p, int nc, int grid, cudaStream_t st) {
   switch (nc) {
-    case 16: return linear::launch<16>(w, p, grid, st);
-    case 32: return linear::launch<32>(w, p, grid, st);
-    case 64: return linear::launch<64>(w, p, grid, st);
-    default: return linear::launch<128>(w, p, grid, st);
+    case 16: return p.M <= 4 ? linear::launch<16, 8>(w, p, grid, st) : linear::launch<16, 16>(w, p, grid, st);
+    case 32: return linear::launch<32, 0>(w, p, grid, st);
+    case 64: return linear::launch<64, 0>(w, p, grid, st);
+    default: return linear::launch<128, 0>(w, p, grid, st);
   }
 }
 

@@ -226,6 +226,7 @@ def test_captured_and_replayed_with_new_inputs(M):
     x, out = L.x(M), torch.empty(M, 1024, device=DEV, dtype=torch.bfloat16)
     ids, wts = torch.empty(M, 6, device=DEV, dtype=torch.int32), torch.empty(M, 6, device=DEV)
     sh = L.shape(M)
+    torch.cuda.synchronize()   # the inputs were made on another stream
     st = torch.cuda.Stream()
     with torch.cuda.stream(st):
         moe.moe_layer_w4(sh, L.weights, x, out, ids, wts, *ws)
@@ -288,6 +289,7 @@ def test_a_decode_step_of_projection_layer_and_logits():
         moe.moe_layer_w4(L.shape(M), L.weights, h, y, ids, wts, *ws)
         moe.moe_linear_w4(sb, y, mats[1][0], None, logits, lw, n)
 
+    torch.cuda.synchronize()   # the inputs were made on another stream
     st = torch.cuda.Stream()
     with torch.cuda.stream(st):
         step()

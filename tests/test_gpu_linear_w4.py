@@ -217,6 +217,7 @@ def test_captured_and_replayed_with_new_inputs(M):
     ws, n = _workspace(sh)
     x = _x(M, K)
     out = torch.empty(M, N, device=DEV)
+    torch.cuda.synchronize()   # the inputs were made on another stream
     st = torch.cuda.Stream()
     with torch.cuda.stream(st):
         moe.moe_linear_w4(sh, x, mat.packed, None, out, ws, n)
