@@ -62,14 +62,15 @@ static int layer_plan(const moe_layer_shape_t& s, LayerPlan* p) {
   if (s.M > 16 || s.E > kMaxE || s.topk > kMaxTopk || s.topk > s.E) return MOE_ERR_UNSUPPORTED;
   if (s.H % 128 || s.I % 128 || s.shared_I % 128 || s.H > 65536 || s.I > 65536 || s.shared_I > 65536)
     return MOE_ERR_UNSUPPORTED;
-  // One layout for every M.  The parts come first, in one place for every
-  // shape: they are zero between calls, the rest is written before it is read.
+  // One layout for every M.  The parts, sigmoids and norm factors come first, in
+  // one place for every shape: they are zero between calls, the rest is written
+  // before it is read.
   size_t o = 256;
   auto take = [&](size_t bytes) { size_t r = o; o = align_up(o + bytes, 256); return r; };
   const size_t KC = s.H / 128, tiles = (size_t)std::min(s.E, 16 * s.topk) * (s.I / 128) + s.shared_I / 128;
   p->o_part1 = take((size_t)kMaxGrid * 32 * 128 * 4);
   p->o_part2 = take((size_t)kMaxGrid * 16 * 128 * 4);
-  p->o_sig = take((size_t)16 * s.E * 4);
+  p->o_sig = take((size_t)16 * kMaxE * 4);
   p->o_rstd = take(16 * 4);
   p->o_xop = take(KC * 32 * 128);
   p->o_xsf = take(KC * 512);
@@ -146,7 +147,8 @@ int moe_linear_w4(const moe_linear_shape_t* shape, const void* x, const void* w_
   LinearParams p = {};
   p.x = static_cast<const uint16_t*>(x);
   p.bias = bias;
-  p.wsf = static_cast<const uint8_t*>(w_packed) + blocks * 8192;
+  p.wcodes = static_cast<const uint8_t*>(w_packed);
+  p.wsf = p.wcodes + blocks * 8192;
   p.out = out;
   p.part = reinterpret_cast<uint32_t*>(ws + kLinearHeader);
   p.status = reinterpret_cast<int32_t*>(ws);
@@ -218,8 +220,8 @@ int moe_layer_w4(const moe_layer_shape_t* shape, const moe_layer_weights_t* w, c
   p.sync = reinterpret_cast<int32_t*>(ws + 64);
   p.part1 = reinterpret_cast<uint32_t*>(ws + pl.o_part1);
   p.part2 = reinterpret_cast<uint32_t*>(ws + pl.o_part2);
-  p.sig = reinterpret_cast<float*>(ws + pl.o_sig);
-  p.rstd = reinterpret_cast<float*>(ws + pl.o_rstd);
+  p.sig = reinterpret_cast<uint32_t*>(ws + pl.o_sig);
+  p.rstd = reinterpret_cast<uint32_t*>(ws + pl.o_rstd);
   p.xop = ws + pl.o_xop; p.xsf = ws + pl.o_xsf;
   p.mop = ws + pl.o_mop; p.msf = ws + pl.o_msf;
   p.ldx = shape->ldx; p.ldo = shape->ldo;

@@ -167,6 +167,7 @@ struct Shares {
 struct LinearParams {
   const uint16_t* x;        // bf16, rows ldx elements apart
   const float* bias;        // may be null
+  const uint8_t* wcodes;    // packed weights, 8192-byte blocks [N/128][K/128]
   const uint8_t* wsf;       // packed weight scales: 512-byte blocks [N/128][K/128]
   uint8_t* xop;             // above 8 tokens: operand blocks and scale blocks [token tile][K/128]
   uint8_t* xsf;
@@ -192,9 +193,9 @@ struct LayerParams {
   int32_t* ids_out;         // [M][topk], or null
   float* wts_out;           // [M][topk], or null
   int32_t* status;
-  int32_t* sync;            // [0] next task, [1] quarters of mid tiles stored; k_layer_head zeroes both
+  int32_t* sync;            // [0] next task, [1] pieces of mid tiles stored; k_layer_head zeroes both
   uint32_t *part1, *part2;  // parts of cut tiles: [grid][gate, up of the tokens][128], [grid][tokens][128]; zero between calls
-  float *sig, *rstd;        // sigmoids of the logits [M][E]; the norm's factors [M]
+  uint32_t *sig, *rstd;     // sigmoids of the logits [M][E], the norm's factors [M], as parts (zero between calls)
   uint8_t *xop, *xsf;       // the tokens' operand blocks and scale blocks [H/128]
   uint8_t *mop, *msf;       // mid's, one per GEMM1 tile
   int64_t ldx, ldo;

@@ -21,7 +21,6 @@
 // only, so the kernel ends however many of its CTAs run at once.  A CTA's
 // weight stream runs ahead into its GEMM2 task while mid is still on its way.
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 #include "w4.cuh"
@@ -131,7 +130,10 @@ __device__ __forceinline__ void split_chunk(const LayerParams& p, int kc) {
 // lane / 4): two MMAs' fragments with K permuted the same way on both sides.
 // The norm weight multiplies the router weight; the product of two 8-bit
 // significands is two bf16 exactly, so nothing is rounded before the sums.
-__global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREADS, 3) k_layer_head(const LayerParams p) {
+// NORM: with the norm; HIGH: more than 8 tokens.  64 registers: two of these
+// blocks leave an SM room for one of k_layer_experts, whose start they overlap.
+template <bool NORM, bool HIGH>
+__global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREADS, HIGH ? 3 : 4) k_layer_head(const LayerParams p) {
   constexpr int BATCH = 3;   // blocks in flight
   {  // the router's rows start for L2 while the kernel before ends
     const int e = blockIdx.x / HEAD_SLICES * 8 + (threadIdx.x >> 2 & 7);
@@ -140,7 +142,10 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
         prefetch_l2_line(p.router_w + (int64_t)e * p.H + b * 32);
   }
   pdl_wait();
-  if (blockIdx.x == 0 && threadIdx.x == 0) { p.sync[0] = 0; p.sync[1] = 0; }
+  if (blockIdx.x + 1 == gridDim.x) {   // before any block of k_layer_experts can start
+    if (threadIdx.x == 0) { p.sync[0] = 0; p.sync[1] = 0; __threadfence(); }
+    __syncthreads();
+  }
   pdl_launch_dependents();
   const int M = p.M, H = p.H, E = p.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nlogit = (E + 7) / 8 * HEAD_SLICES;
@@ -150,12 +155,13 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
   }
   const int eg = blockIdx.x / HEAD_SLICES, slice = blockIdx.x % HEAD_SLICES;
   const int g = lane >> 2, kq = (lane & 3) * 8, nblk = H / 32;
-  const bool e_ok = eg * 8 + g < E, t0 = g < M, t1 = g + 8 < M, norm = p.norm_w != nullptr;
+  const bool e_ok = eg * 8 + g < E, t0 = g < M, t1 = HIGH && g + 8 < M;
   const uint16_t* wr = p.router_w + (int64_t)(e_ok ? eg * 8 + g : 0) * H + kq;
   const uint16_t* x0 = p.x + (int64_t)(t0 ? g : 0) * p.ldx + kq;
   const uint16_t* x1 = p.x + (int64_t)(t1 ? g + 8 : 0) * p.ldx + kq;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   float d[4] = {0.f, 0.f, 0.f, 0.f}, ss0 = 0.0f, ss1 = 0.0f;
+#pragma unroll 1
   for (int b0 = slice * 8 + warp; b0 < nblk; b0 += 8 * HEAD_SLICES * BATCH) {
     uint4 w[BATCH], gw[BATCH], xa[BATCH], xb[BATCH];
 #pragma unroll
@@ -163,15 +169,15 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
       const int b = b0 + i * 8 * HEAD_SLICES;
       const bool in = b < nblk;
       w[i] = in && e_ok ? __ldg(reinterpret_cast<const uint4*>(wr + b * 32)) : zero;
-      gw[i] = in && norm ? __ldg(reinterpret_cast<const uint4*>(p.norm_w + kq + b * 32)) : zero;
+      if (NORM) gw[i] = in ? __ldg(reinterpret_cast<const uint4*>(p.norm_w + kq + b * 32)) : zero;
       xa[i] = in && t0 ? __ldg(reinterpret_cast<const uint4*>(x0 + b * 32)) : zero;
-      xb[i] = in && t1 ? __ldg(reinterpret_cast<const uint4*>(x1 + b * 32)) : zero;
+      xb[i] = HIGH && in && t1 ? __ldg(reinterpret_cast<const uint4*>(x1 + b * 32)) : zero;
     }
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
       const uint32_t a[4] = {xa[i].x, xa[i].y, xa[i].z, xa[i].w}, c[4] = {xb[i].x, xb[i].y, xb[i].z, xb[i].w};
       uint32_t bh[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-      if (norm) {
+      if (NORM) {
         float wf[8], gf[8];
         unpack8(w[i], wf);
         unpack8(gw[i], gf);
@@ -188,9 +194,11 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
         unpack8(xa[i], f);
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss0 = fmaf(f[j], f[j], ss0);
-        unpack8(xb[i], f);
+        if (HIGH) {
+          unpack8(xb[i], f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss1 = fmaf(f[j], f[j], ss1);
+          for (int j = 0; j < 8; ++j) ss1 = fmaf(f[j], f[j], ss1);
+        }
       }
       mma_16816(d, a[0], c[0], a[1], c[1], bh[0], bh[1]);
       mma_16816(d, a[2], c[2], a[3], c[3], bh[2], bh[3]);
@@ -200,14 +208,16 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
   __shared__ float cs[HEAD_SLICES][16 * 8 + 16];   // rank 0's: every slice's sums
   *reinterpret_cast<float2*>(&sd[warp][g][(lane & 3) * 2]) = make_float2(d[0], d[1]);
   *reinterpret_cast<float2*>(&sd[warp][g + 8][(lane & 3) * 2]) = make_float2(d[2], d[3]);
+  if (NORM) {
 #pragma unroll
-  for (int o = 1; o <= 2; o *= 2) {
-    ss0 += __shfl_xor_sync(0xFFFFFFFFu, ss0, o);
-    ss1 += __shfl_xor_sync(0xFFFFFFFFu, ss1, o);
+    for (int o = 1; o <= 2; o *= 2) {
+      ss0 += __shfl_xor_sync(0xFFFFFFFFu, ss0, o);
+      ss1 += __shfl_xor_sync(0xFFFFFFFFu, ss1, o);
+    }
+    if ((lane & 3) == 0) { sq[warp][g] = ss0; sq[warp][g + 8] = ss1; }
   }
-  if ((lane & 3) == 0) { sq[warp][g] = ss0; sq[warp][g + 8] = ss1; }
   __syncthreads();
-  if (threadIdx.x < 128 + 16) {
+  if (threadIdx.x < (NORM ? 128 + 16 : 128)) {
     const int i = threadIdx.x;
     float sum = 0.0f;
 #pragma unroll
@@ -221,32 +231,43 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
   if (t >= M) return;
   float dot = 0.0f, sum = 0.0f, rstd = 1.0f;
 #pragma unroll
-  for (int q = 0; q < HEAD_SLICES; ++q) { dot += cs[q][threadIdx.x]; sum += cs[q][128 + t]; }
-  if (norm) rstd = 1.0f / sqrtf(sum / (float)H + p.eps);
-  if (e < E) p.sig[t * E + e] = sigmoid_spec(dot * rstd);
-  if (eg == 0 && (threadIdx.x & 7) == 0) p.rstd[t] = rstd;
+  for (int q = 0; q < HEAD_SLICES; ++q) { dot += cs[q][threadIdx.x]; sum += NORM ? cs[q][128 + t] : 0.0f; }
+  if (NORM) rstd = 1.0f / sqrtf(sum / (float)H + p.eps);
+  if (e < E) part_put(p.sig + t * E + e, sigmoid_spec(dot * rstd));
+  if (eg == 0 && (threadIdx.x & 7) == 0) part_put(p.rstd + t, rstd);
 }
 
-// Routes token t with one warp from its experts' sigmoids: the top k of sigmoid
-// + bias in k rounds (a tie going to the lower expert), weights as in
-// route_token_warp.  Every CTA runs this once, cold, so the code is kept short.
+// Routes token t with one warp from its experts' sigmoids, which it waits for:
+// the top k of sigmoid + bias in k rounds (a tie going to the lower expert),
+// weights as in route_token_warp.  Every CTA runs this once, cold, so the code
+// is kept short.  False: the wait ran out.
 template <int KPER>
-__device__ __forceinline__ void pick(const LayerParams& p, int t, int* ids, float* wts, uint32_t* mask, float* ssig) {
+__device__ __forceinline__ bool pick(const LayerParams& p, int t, int* ids, float* wts, float* rstd, uint32_t* mask,
+                                     float* ssig, uint64_t deadline) {
   const int lane = threadIdx.x & 31, E = p.E, k = p.topk;
   uint32_t key[KPER];
   {
-    float sg[KPER], bias[KPER];
+    float bias[KPER];
+    uint32_t w[KPER], r = 0;
 #pragma unroll
-    for (int i = 0; i < KPER; ++i) {
-      const int e = lane + 32 * i;
-      sg[i] = e < E ? __ldcg(p.sig + t * E + e) : 0.0f;
-      bias[i] = p.bias && e < E ? __ldg(p.bias + e) : 0.0f;
+    for (int i = 0; i < KPER; ++i) bias[i] = p.bias && lane + 32 * i < E ? __ldg(p.bias + lane + 32 * i) : 0.0f;
+    for (uint32_t spins = 0;;) {
+      r = part_peek(p.rstd + t);
+      bool all = r != 0u;
+#pragma unroll
+      for (int i = 0; i < KPER; ++i) w[i] = lane + 32 * i < E ? part_peek(p.sig + t * E + lane + 32 * i) : 1u;
+#pragma unroll
+      for (int i = 0; i < KPER; ++i) all &= w[i] != 0u;
+      if (__all_sync(0xFFFFFFFFu, all)) break;
+      if ((++spins & 15u) == 0 && globaltimer() > deadline) return false;
     }
 #pragma unroll
     for (int i = 0; i < KPER; ++i) {
-      ssig[lane + 32 * i] = sg[i];
-      key[i] = lane + 32 * i < E ? float_order_key(p.bias ? __fadd_rn(sg[i], bias[i]) : sg[i]) : 0u;
+      const float sg = part_value(w[i]);
+      ssig[lane + 32 * i] = sg;
+      key[i] = lane + 32 * i < E ? float_order_key(p.bias ? __fadd_rn(sg, bias[i]) : sg) : 0u;
     }
+    if (lane == 0) *rstd = part_value(r);
   }
   __syncwarp();
   float denom = 0.0f, mine = 0.0f;
@@ -276,13 +297,14 @@ __device__ __forceinline__ void pick(const LayerParams& p, int t, int* ids, floa
     wts[lane] = __fmul_rn(__fdiv_rn(mine, denom), p.scale);
     atomicOr(mask + (id >> 5), 1u << (id & 31));
   }
+  return true;
 }
 
 // NC: operand columns; TG: tokens a warp's group holds (1 and 2 for as many
 // tokens, else GROUP): the sums of a tile are spread over four warps a group, so
 // that the code is short and a tile's epilogue takes as long for 16 tokens as for 4.
 template <int NC, int TG>
-__global__ void __launch_bounds__(TG == GROUP ? (NC == 32 ? MAX_THREADS : 384) : 256, 1)
+__global__ void __launch_bounds__(TG == GROUP ? (NC == 32 ? MAX_THREADS : 384) : 256, TG == GROUP ? 1 : 2)
 k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant__ CUtensorMap tmW2,
                 const __grid_constant__ CUtensorMap tmS13, const __grid_constant__ CUtensorMap tmS2, const LayerParams p) {
   using C = Cfg<NC>;
@@ -315,18 +337,31 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_wait();   // k_layer_head is done
+  // k_layer_head's blocks are all running: its sigmoids are waited for one by
+  // one, its end (pdl_wait) only by the reader of the operand columns.
   pdl_launch_dependents();
+  const uint64_t deadline = globaltimer() + p.timeout_ns;
+  auto fail = [&](int site) {
+    *abort_flag = 1;
+    atomicOr(p.status, ST_TIMEOUT);
+    atomicCAS(p.status + 2, 0, (int)(0x80000000u | (9u << 24) | ((unsigned)site << 20) | (blockIdx.x & 0xFFFu)));
+  };
   int ticket = 0;
   if (threadIdx.x == 0) ticket = atomicAdd(p.sync, 1);   // in flight while routing runs
   if (warp < M) {   // one token a warp: there are at least M warps
     float* scratch = reinterpret_cast<float*>(abuf) + warp * kMaxE;   // in the idle ring
-    if (E <= 256) pick<8>(p, warp, S.ids + warp * topk, S.wts + warp * topk, S.mask, scratch);
-    else pick<kMaxE / 32>(p, warp, S.ids + warp * topk, S.wts + warp * topk, S.mask, scratch);
-    if (lane == 0) S.rstd[warp] = __ldcg(p.rstd + warp);
+    int* ids = S.ids + warp * topk;
+    float* wts = S.wts + warp * topk;
+    if (!(E <= 256 ? pick<8>(p, warp, ids, wts, S.rstd + warp, S.mask, scratch, deadline)
+                   : pick<kMaxE / 32>(p, warp, ids, wts, S.rstd + warp, S.mask, scratch, deadline)))
+      fail(10);
     fence_proxy_async_smem();   // the ring's next writers are asynchronous copies
   }
   __syncthreads();
+  if (*abort_flag) {   // no routing, no work
+    if (warp == 4) tmem_dealloc(S.tmem, C::TMEM_COLS);
+    return;
+  }
   // the selected experts, ascending: prefix counts of the mask's words, a thread an expert
   const uint32_t mword = lane < kMaxE / 32 ? S.mask[lane] : 0u;
   int ndist;
@@ -343,7 +378,6 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     }
   __syncthreads();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, S.tmem, 0);
-  const uint64_t deadline = globaltimer() + p.timeout_ns;
   // GEMM1: tile i (a gate and an up tile; the shared expert's first) is chunk i
   // of GEMM2's K.  A unit is 128 K of a GEMM1 tile or two chunks of a GEMM2 tile.
   const int tiles1 = JS + ndist * J, CU = (tiles1 + 1) / 2;
@@ -354,11 +388,6 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     if (i < JS) return {0, i, JS, true};
     const int r = i - JS, slot = r / J;
     return {(int)S.dlist[slot], r - slot * J, J, false};
-  };
-  auto fail = [&](int site) {
-    *abort_flag = 1;
-    atomicOr(p.status, ST_TIMEOUT);
-    atomicCAS(p.status + 2, 0, (int)(0x80000000u | (9u << 24) | ((unsigned)site << 20) | (blockIdx.x & 0xFFFu)));
   };
   auto drain = [&]() { const uint64_t until = globaltimer() + 2000000ull; while (globaltimer() < until) { } };
   // Ticket -> product (1, 2; 0: no more tasks), its share and units [u0, u1), units per tile.
@@ -427,6 +456,12 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
       if (!ok) drain();
     }
     __syncwarp();
+    // Every CTA draws one ticket past the tasks.  Whoever draws the last of these
+    // knows that all have routed, and empties what they routed from.
+    if (__shfl_sync(0xFFFFFFFFu, ticket, 0) == sh1.n + sh2.n + G - 1) {
+      for (int i = lane; i < M * E; i += 32) __stcg(p.sig + i, 0u);
+      if (lane < M) __stcg(p.rstd + lane, 0u);
+    }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (the whole warp, one lane issues)
     constexpr uint32_t IDESC = idesc_block_scaled(FMT8_E2M1, FMT8_E4M3, NC);
@@ -495,6 +530,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     uint32_t ph = 0;
     bool ok = true, mid_ready = false;
     Task k;
+    pdl_wait();                   // the tokens' columns are there
     fence_proxy_async_global();   // k_layer_head's stores, read by bulk copies
     for (int n = 0; ok && (ok = next_task(n, &k)); ++n) {
       if (k.gemm == 2 && !mid_ready) {
@@ -538,18 +574,17 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     // Adds the later shares' parts [share + 1, c1] of NV values per row, in K
     // order, to v; value i is token t0 + i % TG's.
     auto live = [&](int i) { return t0 + (i & (TG - 1)) < M; };
-    auto peek = [&](const uint32_t* part, int cb, int c1, auto& w) {   // parts cb .. c1, as many as w holds
-      constexpr int CB = std::extent_v<std::remove_reference_t<decltype(w)>, 0>;
-      constexpr int NV = std::extent_v<std::remove_reference_t<decltype(w)>, 1>;
+    constexpr int CB = 16 / TG;                    // parts in flight
+    auto peek = [&](const uint32_t* part, int cb, int c1, auto& w, auto nv_const) {   // parts cb .. c1, CB at most
+      constexpr int NV = decltype(nv_const)::value;
 #pragma unroll
       for (int c = 0; c < CB; ++c)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
           w[c][i] = live(i) && cb + c <= c1 ? part_peek(part + (cb + c) * (MAX_GROUPS * NV * 128) + i * 128) : 1u;
     };
-    auto gather = [&](uint32_t* part, int share, int c1, auto& v, auto& w) -> bool {   // w: the first batch, peeked
-      constexpr int CB = std::extent_v<std::remove_reference_t<decltype(w)>, 0>;
-      constexpr int NV = std::extent_v<std::remove_reference_t<decltype(w)>, 1>;
+    auto gather = [&](uint32_t* part, int share, int c1, auto& v, auto& w, auto nv_const) -> bool {   // w: the first batch
+      constexpr int NV = decltype(nv_const)::value;
       uint32_t spins = 0;
 #pragma unroll 1
       for (int cb = share + 1; cb <= c1;) {
@@ -575,7 +610,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
           fail(8);
           return false;
         }
-        peek(part, cb, c1, w);
+        peek(part, cb, c1, w, nv_const);
       }
       return true;
     };
@@ -589,9 +624,9 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
         const int c1 = mine ? (k.gemm == 1 ? sh1 : sh2).of(te - 1) : k.share;
         const int b = seg & 1;
         // most parts are there before this share's own sum is: look for them first
-        uint32_t w1[16 / TG][2 * TG], w2[16 / TG][TG];
-        if (k.gemm == 1) peek(part1, k.share + 1, c1, w1);
-        else peek(part2, k.share + 1, c1, w2);
+        uint32_t pw[16 / TG][2 * TG];
+        if (k.gemm == 1) peek(part1, k.share + 1, c1, pw, std::integral_constant<int, 2 * TG>());
+        else peek(part2, k.share + 1, c1, pw, std::integral_constant<int, TG>());
         if (!mbar_wait(&S.accf[b], (seg >> 1) & 1, deadline, abort_flag)) { fail(9); ok = false; break; }
         __syncwarp();
         tc_fence_after();
@@ -630,7 +665,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
                 for (int t = 0; t < TG; ++t)
                   if (live(t) && S.ids[(t0 + t) * topk + j] == w.e) wt[t] = S.wts[(t0 + t) * topk + j];
             }
-            if (!gather(part1, k.share, c1, v, w1)) { ok = false; break; }
+            if (!gather(part1, k.share, c1, v, pw, std::integral_constant<int, 2 * TG>())) { ok = false; break; }
             float m[TG];
             int s[TG];
 #pragma unroll
@@ -676,7 +711,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
 #pragma unroll
             for (int t = 0; t < TG; ++t)
               r[t] = p.residual && live(t) ? __uint_as_float((uint32_t)__ldg(p.x + (t0 + t) * p.ldx + h) << 16) : 0.0f;
-            if (!gather(part2, k.share, c1, v, w2)) { ok = false; break; }
+            if (!gather(part2, k.share, c1, v, pw, std::integral_constant<int, TG>())) { ok = false; break; }
 #pragma unroll
             for (int t = 0; t < TG; ++t)
               if (live(t)) p.out[(t0 + t) * p.ldo + h] = bf16_bits(v[t] + r[t]);
@@ -711,28 +746,31 @@ static cudaLaunchConfig_t config(int grid, int threads, int smem, cudaStream_t s
 
 template <int NC, int TG>
 static cudaError_t launch_experts(const CUtensorMap* m, const LayerParams& p, int grid, cudaStream_t st) {
-  static std::atomic<uint64_t> ready{0};   // devices on which the kernel may take its shared memory
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = set_up_kernel(k_layer_experts<NC, TG>, smem_bytes<NC>(), &ready);
   if (e != cudaSuccess) return e;
-  if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
-    e = cudaFuncSetAttribute(k_layer_experts<NC, TG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NC>());
-    if (e != cudaSuccess) return e;
-    if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
-  }
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = config(grid, 128 + 128 * ((p.M + TG - 1) / TG), smem_bytes<NC>(), st, &attr);
   return cudaLaunchKernelEx(&cfg, k_layer_experts<NC, TG>, m[0], m[1], m[2], m[3], p);
+}
+
+template <bool NORM, bool HIGH>
+static cudaError_t launch_head(const LayerParams& p, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = set_up_kernel(k_layer_head<NORM, HIGH>, 0, &ready);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  const int chunks = (p.H / 128 + HEAD_SLICES - 1) / HEAD_SLICES * HEAD_SLICES;   // whole clusters
+  const cudaLaunchConfig_t cfg = config((p.E + 7) / 8 * HEAD_SLICES + chunks, HEAD_THREADS, 0, st, &attr);
+  return cudaLaunchKernelEx(&cfg, k_layer_head<NORM, HIGH>, p);
 }
 
 }  // namespace layer
 
 cudaError_t launch_layer_w4(const CUtensorMap* maps, const LayerParams& p, int sms, cudaStream_t st) {
   using namespace layer;
-  cudaLaunchAttribute attr;
-  const int chunks = (p.H / 128 + HEAD_SLICES - 1) / HEAD_SLICES * HEAD_SLICES;   // whole clusters
-  const cudaLaunchConfig_t cfg = config((p.E + 7) / 8 * HEAD_SLICES + chunks, HEAD_THREADS, 0, st, &attr);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_layer_head, p);
+  const cudaError_t e = p.norm_w ? (p.M > 8 ? launch_head<true, true>(p, st) : launch_head<true, false>(p, st))
+                                 : (p.M > 8 ? launch_head<false, true>(p, st) : launch_head<false, false>(p, st));
   if (e != cudaSuccess) return e;
   if (p.M == 1) return launch_experts<16, 1>(maps, p, sms, st);
   if (p.M == 2) return launch_experts<16, 2>(maps, p, sms, st);

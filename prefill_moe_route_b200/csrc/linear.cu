@@ -14,8 +14,6 @@
 // warp for each token splits its K chunks into the operand ring (above 8 tokens
 // k_split_x does it before, and the stream brings them), one thread issues the
 // MMAs, four warps for each 16 tokens read the sums out of TMEM.
-#include <atomic>
-
 #include "w4.cuh"
 
 namespace moe {
@@ -25,6 +23,7 @@ using namespace w4;
 
 constexpr int WARP_SPLIT0 = 2;
 constexpr int UK = 2;               // K chunks of 128 in a unit
+constexpr int AHEAD = 5;            // units of a share sent for L2 before the kernel may read: one round of the ring
 constexpr int SF_SLOTS = 4;         // TMEM scale slots: per chunk 4 columns of weight scales + 4 of token scales
 
 // NC: operand columns, two per token.  SW: warps that split the tokens' K chunks
@@ -82,6 +81,21 @@ __device__ __forceinline__ void split_item(const uint4& u, uint8_t* tile, uint8_
   }
 }
 
+// A share's first units start for L2 while the kernel before this call ends (a
+// prefetch only: what that kernel writes stays what is read).  1 x 6144 x 6144:
+// 7.4 us without, 6.8 with.
+__device__ __forceinline__ void prefetch_weights(const LinearParams& p, int share) {
+  const int u0 = p.shares.begin(share), n = min(p.shares.begin(share + 1) - u0, AHEAD);
+  int tile = u0 / p.KU, ku = u0 - tile * p.KU;
+  for (int i = 0; i < n; ++i) {
+    const int64_t blk = (int64_t)(tile / p.TT) * p.KC + ku * UK;
+    const int nk = min(UK, p.KC - ku * UK);
+    prefetch_l2_bulk(p.wcodes + blk * CODE_BLOCK, nk * CODE_BLOCK);
+    prefetch_l2_bulk(p.wsf + blk * SF_BLOCK, nk * SF_BLOCK);
+    if (++ku == p.KU) { ku = 0; ++tile; }
+  }
+}
+
 template <int NC, int SW>
 __global__ void __launch_bounds__(Cfg<NC, SW>::THREADS, 1)
 k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
@@ -113,7 +127,10 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
     S.abort_flag = 0;
     fence_mbar_init();
   }
-  if (threadIdx.x == 32) tma_prefetch_desc(&tmW);
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&tmW);
+    if (!C::PRE) prefetch_weights(p, share);
+  }
   if (warp == WARP_EPI0) { tmem_alloc(&S.tmem, C::TMEM_COLS); tmem_relinquish(); }
   tc_fence_before();
   __syncthreads();
@@ -396,15 +413,9 @@ __global__ void __launch_bounds__(256) k_split_x(const LinearParams p) {
 
 template <int NC, int SW>
 static cudaError_t launch(const CUtensorMap& w, const LinearParams& p, int grid, cudaStream_t st) {
-  static std::atomic<uint64_t> ready{0};   // devices on which the kernel may take its shared memory
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = set_up_kernel(k_linear_w4<NC, SW>, smem_bytes<NC, SW>(), &ready);
   if (e != cudaSuccess) return e;
-  if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
-    e = cudaFuncSetAttribute(k_linear_w4<NC, SW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NC, SW>());
-    if (e != cudaSuccess) return e;
-    if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
-  }
   // The kernel's set-up may overlap the tail of the call before it.
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -421,6 +432,8 @@ static cudaError_t launch(const CUtensorMap& w, const LinearParams& p, int grid,
     pre.gridDim = dim3(p.KC, (p.M + 15) / 16);
     pre.blockDim = dim3(256);
     pre.dynamicSmemBytes = 0;
+    static std::atomic<uint64_t> pre_ready{0};
+    if ((e = set_up_kernel(k_split_x<NC>, 0, &pre_ready)) != cudaSuccess) return e;
     if ((e = cudaLaunchKernelEx(&pre, k_split_x<NC>, p)) != cudaSuccess) return e;
   }
   return cudaLaunchKernelEx(&cfg, k_linear_w4<NC, SW>, w, p);

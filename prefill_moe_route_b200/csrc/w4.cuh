@@ -16,6 +16,8 @@
 // A block that holds an infinity or a NaN becomes NaN in both columns, so only
 // its own token's sums become NaN.
 #pragma once
+#include <atomic>
+
 #include "internal.h"
 #include "ptx.cuh"
 #include "codec.cuh"
@@ -94,6 +96,21 @@ __device__ __forceinline__ uint32_t part_peek(const uint32_t* p) {
   return v;
 }
 __device__ __forceinline__ float part_value(uint32_t word) { return __uint_as_float(~word); }
+
+// Once per device and kernel: its dynamic shared memory, and the split of the
+// SM's memory towards shared memory, without which a small kernel cannot run
+// beside one of these large ones (the SM would have to be empty to change it).
+template <typename Kernel>
+inline cudaError_t set_up_kernel(Kernel* kernel, int smem, std::atomic<uint64_t>* ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev <= 63 && (ready->load(std::memory_order_relaxed) >> dev & 1u)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && smem) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && dev <= 63) ready->fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
 
 }  // namespace w4
 }  // namespace moe
