@@ -155,6 +155,7 @@ struct Shares {
   int n, base, rem;
   MOE_HD Shares() {}
   MOE_HD Shares(int total, int count) : n(count), base(total / count), rem(total % count) {}
+  MOE_HD Shares(int count, int quotient, int remainder) : n(count), base(quotient), rem(remainder) {}
   MOE_HD int begin(int c) const { return c * base + (c < rem ? c : rem); }
   MOE_HD int of(int u) const {
     const int big = rem * (base + 1);

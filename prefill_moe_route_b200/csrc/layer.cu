@@ -34,7 +34,7 @@ constexpr int HEAD_THREADS = 256;
 constexpr int HEAD_SLICES = 8;     // CTAs along K of 8 experts' logits
 constexpr int GROUP = 4;           // tokens whose sums one warp keeps
 constexpr int MAX_GROUPS = 4;
-// warps: 0 weights, 1 MMA, 2 operands, 3 routing only, then four a group of tokens for the sums
+// warps: 0 weights, 1 MMA, 2 operands, 3 routing, then four a group of tokens for the sums
 constexpr int MAX_THREADS = 128 + 128 * MAX_GROUPS;
 constexpr int STAGES = 5;
 constexpr int SF_SLOTS = 4;        // TMEM scale slots of 16 columns: two weight blocks, two operand blocks
@@ -63,6 +63,7 @@ struct Smem {
   int ids[MAX_M * kMaxTopk];
   float wts[MAX_M * kMaxTopk];
   uint32_t mask[kMaxE / 32];       // selected experts
+  alignas(16) uint8_t choice[kMaxE][MAX_M];   // by expert and token: 1 + which choice of the token's, 0: none
   uint16_t dlist[MAX_SLOTS];
 };
 
@@ -141,6 +142,20 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
       for (int b = blockIdx.x % HEAD_SLICES * 8 + (threadIdx.x >> 5); b < p.H / 32; b += 8 * HEAD_SLICES)
         prefetch_l2_line(p.router_w + (int64_t)e * p.H + b * 32);
   }
+  __shared__ float sd[8][16][8], sq[8][16];
+  __shared__ float cs[HEAD_SLICES][16 * 8 + 16];   // rank 0's: every slice's sums
+  __shared__ uint64_t arrived;                     // rank 0's: their bytes
+  const int nlogit = (p.E + 7) / 8 * HEAD_SLICES;
+  const bool logits = blockIdx.x < nlogit;         // the same for a whole cluster
+  if (logits) {
+    if (threadIdx.x == 0) {
+      mbar_init(&arrived, 1);
+      fence_mbar_init();
+      mbar_arrive_expect_tx(&arrived, HEAD_SLICES * (NORM ? 144 : 128) * 4);
+    }
+    __syncthreads();
+    cluster_arrive_release();   // ready for the others' stores (waited for before they are made)
+  }
   pdl_wait();
   if (blockIdx.x + 1 == gridDim.x) {   // before any block of k_layer_experts can start
     if (threadIdx.x == 0) { p.sync[0] = 0; p.sync[1] = 0; __threadfence(); }
@@ -148,8 +163,8 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
   }
   pdl_launch_dependents();
   const int M = p.M, H = p.H, E = p.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nlogit = (E + 7) / 8 * HEAD_SLICES;
-  if (blockIdx.x >= nlogit) {   // a whole cluster
+  const uint64_t deadline = globaltimer() + p.timeout_ns;
+  if (!logits) {
     if (blockIdx.x - nlogit < H / 128) split_chunk(p, blockIdx.x - nlogit);
     return;
   }
@@ -204,8 +219,6 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
       mma_16816(d, a[2], c[2], a[3], c[3], bh[2], bh[3]);
     }
   }
-  __shared__ float sd[8][16][8], sq[8][16];
-  __shared__ float cs[HEAD_SLICES][16 * 8 + 16];   // rank 0's: every slice's sums
   *reinterpret_cast<float2*>(&sd[warp][g][(lane & 3) * 2]) = make_float2(d[0], d[1]);
   *reinterpret_cast<float2*>(&sd[warp][g + 8][(lane & 3) * 2]) = make_float2(d[2], d[3]);
   if (NORM) {
@@ -217,16 +230,17 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
     if ((lane & 3) == 0) { sq[warp][g] = ss0; sq[warp][g + 8] = ss1; }
   }
   __syncthreads();
+  cluster_wait_acquire();
   if (threadIdx.x < (NORM ? 128 + 16 : 128)) {
     const int i = threadIdx.x;
     float sum = 0.0f;
 #pragma unroll
     for (int q = 0; q < 8; ++q) sum += i < 128 ? sd[q][i >> 3][i & 7] : sq[q][i - 128];
-    st_shared_cluster_f32(mapa_shared(smem_u32(&cs[slice][i]), 0), sum);
+    st_async_cluster_f32(mapa_shared(smem_u32(&cs[slice][i]), 0), sum, mapa_shared(smem_u32(&arrived), 0));
   }
-  cluster_arrive_release();
-  cluster_wait_acquire();   // rank 0's shared memory outlives the stores: it leaves last
   if (slice != 0 || threadIdx.x >= 128) return;
+  for (uint32_t spins = 0; !mbar_try_wait_cluster(&arrived, 0);)   // bounded: k_layer_experts then finds nothing and says so
+    if ((++spins & 255u) == 0 && globaltimer() > deadline) return;
   const int t = threadIdx.x >> 3, e = eg * 8 + (threadIdx.x & 7);
   if (t >= M) return;
   float dot = 0.0f, sum = 0.0f, rstd = 1.0f;
@@ -243,7 +257,7 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
 // is kept short.  False: the wait ran out.
 template <int KPER>
 __device__ __forceinline__ bool pick(const LayerParams& p, int t, int* ids, float* wts, float* rstd, uint32_t* mask,
-                                     float* ssig, uint64_t deadline) {
+                                     uint8_t* choice, float* ssig, uint64_t deadline) {
   const int lane = threadIdx.x & 31, E = p.E, k = p.topk;
   uint32_t key[KPER];
   {
@@ -295,6 +309,7 @@ __device__ __forceinline__ bool pick(const LayerParams& p, int t, int* ids, floa
   if (lane < k) {
     ids[lane] = id;
     wts[lane] = __fmul_rn(__fdiv_rn(mine, denom), p.scale);
+    choice[id * MAX_M + t] = static_cast<uint8_t>(lane + 1);
     atomicOr(mask + (id >> 5), 1u << (id & 31));
   }
   return true;
@@ -334,6 +349,8 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
   }
   if (warp == 4) { tmem_alloc(&S.tmem, C::TMEM_COLS); tmem_relinquish(); }
   if (threadIdx.x >= 64 && threadIdx.x < 64 + kMaxE / 32) S.mask[threadIdx.x - 64] = 0u;
+  for (int i = threadIdx.x; i < E; i += blockDim.x)
+    reinterpret_cast<uint4*>(S.choice)[i] = make_uint4(0u, 0u, 0u, 0u);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -352,8 +369,8 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     float* scratch = reinterpret_cast<float*>(abuf) + warp * kMaxE;   // in the idle ring
     int* ids = S.ids + warp * topk;
     float* wts = S.wts + warp * topk;
-    if (!(E <= 256 ? pick<8>(p, warp, ids, wts, S.rstd + warp, S.mask, scratch, deadline)
-                   : pick<kMaxE / 32>(p, warp, ids, wts, S.rstd + warp, S.mask, scratch, deadline)))
+    if (!(E <= 256 ? pick<8>(p, warp, ids, wts, S.rstd + warp, S.mask, S.choice[0], scratch, deadline)
+                   : pick<kMaxE / 32>(p, warp, ids, wts, S.rstd + warp, S.mask, S.choice[0], scratch, deadline)))
       fail(10);
     fence_proxy_async_smem();   // the ring's next writers are asynchronous copies
   }
@@ -371,22 +388,21 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     const int n = __shfl_sync(0xFFFFFFFFu, before, i) + __popc(m & ((1u << lane) - 1u));
     if ((m >> lane) & 1u) S.dlist[n] = static_cast<uint16_t>(32 * i + lane);
   }
-  if (blockIdx.x == 0)
-    for (int q = threadIdx.x; q < M * topk; q += blockDim.x) {
-      if (p.ids_out) p.ids_out[q] = S.ids[q];
-      if (p.wts_out) p.wts_out[q] = S.wts[q];
-    }
   __syncthreads();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, S.tmem, 0);
   // GEMM1: tile i (a gate and an up tile; the shared expert's first) is chunk i
   // of GEMM2's K.  A unit is 128 K of a GEMM1 tile or two chunks of a GEMM2 tile.
   const int tiles1 = JS + ndist * J, CU = (tiles1 + 1) / 2;
   const int U1 = tiles1 * KC, U2 = HT * CU, G = gridDim.x;
-  const Shares sh1(U1, min(G, (U1 + MIN_SHARE - 1) / MIN_SHARE)), sh2(U2, min(G, (U2 + MIN_SHARE - 1) / MIN_SHARE));
+  auto cut = [&](int units) -> Shares {
+    const int n = min(G, (units + MIN_SHARE - 1) / MIN_SHARE), q = quick_div(units, n);
+    return Shares(n, q, units - q * n);
+  };
+  const Shares sh1 = cut(U1), sh2 = cut(U2);
   struct Where { int e, j, iw; bool shared; };
   auto where = [&](int i) -> Where {
     if (i < JS) return {0, i, JS, true};
-    const int r = i - JS, slot = r / J;
+    const int r = i - JS, slot = quick_div(r, J);
     return {(int)S.dlist[slot], r - slot * J, J, false};
   };
   auto drain = [&]() { const uint64_t until = globaltimer() + 2000000ull; while (globaltimer() < until) { } };
@@ -421,7 +437,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
         const Task k = task_of(ticket);
         if (!k.gemm) break;
         ticket = atomicAdd(p.sync, 1);
-        int tile = k.u0 / k.len, i = k.u0 - tile * k.len;
+        int tile = quick_div(k.u0, k.len), i = k.u0 - tile * k.len;
         Where w = where(k.gemm == 1 ? tile : 0);
         for (int u = k.u0; u < k.u1; ++u) {
           if (!mbar_wait(&S.empty[st], ph ^ 1, deadline, abort_flag)) { fail(3); ok = false; break; }
@@ -470,7 +486,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     bool ok = true;
     Task k;
     for (int n = 0; ok && (ok = next_task(n, &k)); ++n) {
-      int i = k.u0 % k.len;
+      int i = k.u0 - quick_div(k.u0, k.len) * k.len;
       bool first = true;
       const int nu = k.u1 - k.u0;
       const bool one = k.gemm == 1;
@@ -545,7 +561,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
         mid_ready = true;
       }
       if (lane == 0) {
-        int i = k.u0 % k.len;
+        int i = k.u0 - quick_div(k.u0, k.len) * k.len;
         for (int u = k.u0; u < k.u1; ++u) {
           if (!mbar_wait(&S.empty[st], ph ^ 1, deadline, abort_flag)) { fail(7); ok = false; break; }
           const int nk = k.gemm == 1 ? 1 : min(2, tiles1 - 2 * i);
@@ -563,7 +579,13 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     }
     if (*abort_flag) drain();
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp == 3) {
+    if (blockIdx.x == 0)
+      for (int q = lane; q < M * topk; q += 32) {
+        if (p.ids_out) p.ids_out[q] = S.ids[q];
+        if (p.wts_out) p.wts_out[q] = S.wts[q];
+      }
+  } else {
     // ------------------------------------------------ sums
     const int q = warp & 3, row = 32 * q + lane;   // TMEM lane quarter = warp % 4
     const int t0 = (warp - 4) / 4 * TG;            // this warp's tokens t0 .. t0 + TG - 1
@@ -619,7 +641,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     uint32_t* part2 = p.part2 + t0 * 128 + row;
     for (int n = 0; ok && next_task(n, &k); ++n) {
       for (int u = k.u0; u < k.u1 && ok; ++seg) {
-        const int tile = u / k.len, tb = tile * k.len, te = tb + k.len, ue = min(te, k.u1);
+        const int tile = quick_div(u, k.len), tb = tile * k.len, te = tb + k.len, ue = min(te, k.u1);
         const bool mine = u == tb;   // this share starts the tile and so finishes it
         const int c1 = mine ? (k.gemm == 1 ? sh1 : sh2).of(te - 1) : k.share;
         const int b = seg & 1;
@@ -659,11 +681,11 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
 #pragma unroll
             for (int t = 0; t < TG; ++t) wt[t] = w.shared && live(t) ? 1.0f : 0.0f;
             if (!w.shared) {
-#pragma unroll 1
-              for (int j = 0; j < topk; ++j)
 #pragma unroll
-                for (int t = 0; t < TG; ++t)
-                  if (live(t) && S.ids[(t0 + t) * topk + j] == w.e) wt[t] = S.wts[(t0 + t) * topk + j];
+              for (int t = 0; t < TG; ++t) {
+                const int c = S.choice[w.e][(t0 + t) & (MAX_M - 1)];
+                if (c) wt[t] = S.wts[(t0 + t) * topk + c - 1];
+              }
             }
             if (!gather(part1, k.share, c1, v, pw, std::integral_constant<int, 2 * TG>())) { ok = false; break; }
             float m[TG];

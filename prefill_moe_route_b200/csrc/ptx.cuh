@@ -132,8 +132,12 @@ __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t cluster_saddr) {
   return v;
 }
 
-__device__ __forceinline__ void st_shared_cluster_f32(uint32_t cluster_saddr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_saddr), "f"(v) : "memory");
+// Store to a CTA of the cluster that completes 4 bytes of transaction count on a
+// barrier of the same CTA: the value and its arrival in one trip.
+__device__ __forceinline__ void st_async_cluster_f32(uint32_t cluster_saddr, float v, uint32_t cluster_bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(cluster_saddr), "f"(v),
+               "r"(cluster_bar)
+               : "memory");
 }
 
 // ------------------------------------------------------------ global flags

@@ -82,6 +82,16 @@ __device__ __forceinline__ uint32_t tile_byte(uint32_t n, uint32_t k) {
 // Byte of row n's scale of group q (0..3) in a 512-byte scale block.
 __device__ __forceinline__ uint32_t sf_byte(uint32_t n, uint32_t q) { return 16u * (n & 31u) + 4u * (n >> 5) + q; }
 
+// a / b for 0 <= a < 2^31, b > 0, through the fp32 quotient (a few off at most):
+// integer divisions follow one another where a kernel works out its share.
+__device__ __forceinline__ int quick_div(int a, int b) {
+  int q = __float2int_rz(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+  int r = a - q * b;
+  while (r < 0) { --q; r += b; }
+  while (r >= b) { ++q; r -= b; }
+  return q;
+}
+
 // A part of a sum on its way to another CTA: the word is the value's bits
 // inverted, so that zero (what the buffer holds between calls) marks a part
 // that has not arrived.  Value and arrival are one 4-byte word: no fence, no
