@@ -337,13 +337,18 @@ MOE_API int moe_quantize_fp8_block128(const float* w, int64_t batch, int32_t row
  * weights is quantized; the calls above quantize the activations too).  Sums
  * are fp32.  An infinity or a NaN in a token's row makes that token's outputs
  * NaN and leaves the other tokens' alone; a subnormal activation (below 2^-126)
- * counts as zero.  Results do not depend on timing:
- * the same call gives the same bits.                                        */
+ * counts as zero.  Weight scales are finite (code 255 is not looked for).
+ * Results do not depend on timing: the same call gives the same bits.
+ *
+ * The kernels of a call are launched so that their set-up overlaps the end of
+ * the kernel before them in the stream (programmatic dependent launch); what
+ * that kernel wrote is read only after it has ended.                        */
 
 enum { MOE_OUT_BF16 = 0, MOE_OUT_F32 = 1 };
 
-/* out[m][n] = sum_k x[m][k] * W[n][k] (+ bias[n]).  M >= 1 tokens (meant for a
- * few; any number works), N >= 1 rows of weights, K % 32 == 0.
+/* out[m][n] = sum_k x[m][k] * W[n][k] (+ bias[n]).  1 <= M <= 2^19 tokens (meant
+ * for a few), 1 <= N <= 2^24 rows of weights, 32 <= K <= 2^20, K % 32 == 0, and
+ * ceil(N/128) * ceil(K/128) < 2^24.
  *   ldx, ldo   elements between rows of x and of out (ldx >= K, ldx % 8 == 0;
  *              ldo >= N); columns past K and N are neither read nor written
  *   out_type   MOE_OUT_BF16 (rounded once) or MOE_OUT_F32                    */
@@ -381,8 +386,9 @@ MOE_API int moe_linear_w4(const moe_linear_shape_t* shape, const void* x, const 
  *   y      = sum_j w_j * E_j(h) + E_shared(h),
  *            E(h) = (silu(h . gate^T) * (h . up^T)) . down^T
  *   out    = bf16( y (+ x with add_residual) )
- * h is not rounded for the router (fp32 products); for the experts h and the
- * SwiGLU output are held to 2^-9 of each value (h is exact without a norm).
+ * h is not rounded for the router (fp32 sums, mean(x^2) in fp32 too); for the
+ * experts h and the SwiGLU output are held to 2^-9 of each value (h is exact
+ * without a norm).
  * H, I, shared_I multiples of 128 (shared_I 0: no shared expert), E <= 512,
  * topk <= min(E, 16); ldx, ldo: elements between rows (>= H, ldx % 8 == 0).  */
 typedef struct {

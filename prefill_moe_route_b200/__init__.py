@@ -46,6 +46,7 @@ _NAMES = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED", -3:
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libmoe_b200.so")
 _lib = None
+_current = None   # query of torch's current stream, set up at the first use
 
 
 class MoeError(RuntimeError):
@@ -163,18 +164,28 @@ def load():
 def _ptr(t):
     if t is None:
         return None
-    if isinstance(t, int):
+    try:
+        return t.data_ptr()
+    except AttributeError:   # an integer device address
         return t
-    return t.data_ptr()
+
+
+def _current_stream():
+    """torch's current stream; the raw query costs 0.2 us, torch.cuda.current_stream() 3 us."""
+    import torch
+    try:
+        get, dev = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    except AttributeError:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: get(dev())
 
 
 def _stream(s):
-    if s is None:   # torch's current stream; the raw query costs 0.2 us, torch.cuda.current_stream() 3 us
-        import torch
-        try:
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-        except AttributeError:
-            return torch.cuda.current_stream().cuda_stream
+    global _current
+    if s is None:
+        if _current is None:
+            _current = _current_stream()
+        return _current()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -342,9 +353,9 @@ def moe_linear_w4_workspace_size(shape: MoeLinearShape) -> int:
 def moe_linear_w4(shape: MoeLinearShape, x, w_packed, bias, out, workspace, ws_bytes: int, stream=None,
                   check: bool = True) -> int:
     """out = x W^T (+ bias) for few tokens: MXFP4 weights, bf16 activations kept as they are, fp32 sums."""
-    rc = load().moe_linear_w4(ctypes.byref(shape), _ptr(x), _ptr(w_packed), _ptr(bias), _ptr(out), _ptr(workspace),
-                              ws_bytes, _stream(stream))
-    return _ret(rc, "moe_linear_w4", check)
+    rc = (_lib or load()).moe_linear_w4(ctypes.byref(shape), _ptr(x), _ptr(w_packed), _ptr(bias), _ptr(out),
+                                        _ptr(workspace), ws_bytes, _stream(stream))
+    return rc if rc == MOE_OK else _ret(rc, "moe_linear_w4", check)
 
 
 def moe_layer_w4_workspace_size(shape: MoeLayerShape) -> int:
@@ -356,6 +367,6 @@ def moe_layer_w4_workspace_size(shape: MoeLayerShape) -> int:
 def moe_layer_w4(shape: MoeLayerShape, weights: MoeLayerWeights, x, out, topk_ids, topk_w, workspace, ws_bytes: int,
                  stream=None, check: bool = True) -> int:
     """A whole MoE layer for a few tokens: norm, router, top-k, experts, shared expert, residual."""
-    rc = load().moe_layer_w4(ctypes.byref(shape), ctypes.byref(weights), _ptr(x), _ptr(out), _ptr(topk_ids),
-                             _ptr(topk_w), _ptr(workspace), ws_bytes, _stream(stream))
-    return _ret(rc, "moe_layer_w4", check)
+    rc = (_lib or load()).moe_layer_w4(ctypes.byref(shape), ctypes.byref(weights), _ptr(x), _ptr(out), _ptr(topk_ids),
+                                       _ptr(topk_w), _ptr(workspace), ws_bytes, _stream(stream))
+    return rc if rc == MOE_OK else _ret(rc, "moe_layer_w4", check)

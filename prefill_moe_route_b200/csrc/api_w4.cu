@@ -29,7 +29,7 @@ static int linear_plan(const moe_linear_shape_t& s, int sms, LinearPlan* p) {
   if (s.M < 1 || s.N < 1 || s.K < 32 || s.K % 32) return MOE_ERR_INVALID_ARG;
   if (s.ldx < s.K || s.ldo < s.N || s.ldx % 8) return MOE_ERR_INVALID_ARG;
   if (s.out_type != MOE_OUT_BF16 && s.out_type != MOE_OUT_F32) return MOE_ERR_INVALID_ARG;
-  if (s.M > (1 << 20) || s.K > (1 << 20) || s.N > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  if (s.M > (1 << 19) || s.K > (1 << 20) || s.N > (1 << 24)) return MOE_ERR_UNSUPPORTED;
   p->RT = (s.N + 127) / 128;
   p->KC = (s.K + 127) / 128;
   p->KU = (p->KC + 1) / 2;                 // a unit is two chunks
@@ -105,6 +105,10 @@ int moe_pack_w4(const uint8_t* q, const uint8_t* scales, int32_t N, int32_t K, u
   if (moe_w4_packed_size(N, K, &bytes) != MOE_OK) return fail(MOE_ERR_INVALID_ARG, "moe_pack_w4: N < 1 or K not a multiple of 32");
   if ((int64_t)(bytes / 8704) * 128 > INT_MAX) return fail(MOE_ERR_UNSUPPORTED, "moe_pack_w4: matrix too large");
   if (!aligned(q, 16) || !aligned(packed, 256)) return fail(MOE_ERR_INVALID_ARG, "moe_pack_w4: q needs 16-byte, packed 256-byte alignment");
+  const uintptr_t p0 = reinterpret_cast<uintptr_t>(packed), p1 = p0 + bytes, q0 = reinterpret_cast<uintptr_t>(q),
+                  s0 = reinterpret_cast<uintptr_t>(scales), n = N;
+  if ((q0 < p1 && p0 < q0 + n * (K / 2)) || (s0 < p1 && p0 < s0 + n * (K / 32)))
+    return fail(MOE_ERR_INVALID_ARG, "moe_pack_w4: buffers overlap");
   const void* ptrs[3] = {q, scales, packed};
   const int dev = resolve_device(stream, ptrs, 3);
   if (dev < 0) return dev;

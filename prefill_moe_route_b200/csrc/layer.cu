@@ -30,6 +30,10 @@ namespace layer {
 
 using namespace w4;
 
+// What other kernels may write is read through L2 (__ldcg) throughout: these
+// blocks can be resident, beside others that fill their SM's L1, long before
+// the kernel whose results they wait for has ended.
+
 constexpr int HEAD_THREADS = 256;
 constexpr int HEAD_SLICES = 8;     // CTAs along K of 8 experts' logits
 constexpr int GROUP = 4;           // tokens whose sums one warp keeps
@@ -94,10 +98,10 @@ __device__ __forceinline__ void split_chunk(const LayerParams& p, int kc) {
   const int t = threadIdx.x >> 4, g8 = threadIdx.x & 15, k = kc * 128 + g8 * 8;
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (t < p.M) {
-    unpack8(__ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.ldx + k)), v);
+    unpack8(__ldcg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.ldx + k)), v);
     if (p.norm_w) {
       float g[8];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(p.norm_w + k)), g);
+      unpack8(__ldcg(reinterpret_cast<const uint4*>(p.norm_w + k)), g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= g[i];
     }
@@ -183,10 +187,10 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
     for (int i = 0; i < BATCH; ++i) {
       const int b = b0 + i * 8 * HEAD_SLICES;
       const bool in = b < nblk;
-      w[i] = in && e_ok ? __ldg(reinterpret_cast<const uint4*>(wr + b * 32)) : zero;
-      if (NORM) gw[i] = in ? __ldg(reinterpret_cast<const uint4*>(p.norm_w + kq + b * 32)) : zero;
-      xa[i] = in && t0 ? __ldg(reinterpret_cast<const uint4*>(x0 + b * 32)) : zero;
-      xb[i] = HIGH && in && t1 ? __ldg(reinterpret_cast<const uint4*>(x1 + b * 32)) : zero;
+      w[i] = in && e_ok ? __ldcg(reinterpret_cast<const uint4*>(wr + b * 32)) : zero;
+      if (NORM) gw[i] = in ? __ldcg(reinterpret_cast<const uint4*>(p.norm_w + kq + b * 32)) : zero;
+      xa[i] = in && t0 ? __ldcg(reinterpret_cast<const uint4*>(x0 + b * 32)) : zero;
+      xb[i] = HIGH && in && t1 ? __ldcg(reinterpret_cast<const uint4*>(x1 + b * 32)) : zero;
     }
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
@@ -264,7 +268,7 @@ __device__ __forceinline__ bool pick(const LayerParams& p, int t, int* ids, floa
     float bias[KPER];
     uint32_t w[KPER], r = 0;
 #pragma unroll
-    for (int i = 0; i < KPER; ++i) bias[i] = p.bias && lane + 32 * i < E ? __ldg(p.bias + lane + 32 * i) : 0.0f;
+    for (int i = 0; i < KPER; ++i) bias[i] = p.bias && lane + 32 * i < E ? __ldcg(p.bias + lane + 32 * i) : 0.0f;
     for (uint32_t spins = 0;;) {
       r = part_peek(p.rstd + t);
       bool all = r != 0u;
@@ -732,7 +736,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
             float r[TG];
 #pragma unroll
             for (int t = 0; t < TG; ++t)
-              r[t] = p.residual && live(t) ? __uint_as_float((uint32_t)__ldg(p.x + (t0 + t) * p.ldx + h) << 16) : 0.0f;
+              r[t] = p.residual && live(t) ? __uint_as_float((uint32_t)__ldcg(p.x + (t0 + t) * p.ldx + h) << 16) : 0.0f;
             if (!gather(part2, k.share, c1, v, pw, std::integral_constant<int, TG>())) { ok = false; break; }
 #pragma unroll
             for (int t = 0; t < TG; ++t)

@@ -21,6 +21,9 @@ namespace linear {
 
 using namespace w4;
 
+// x and bias are read through L2 (__ldcg): a block can be resident before the
+// kernel that writes them has ended.
+
 constexpr int WARP_SPLIT0 = 2;
 constexpr int UK = 2;               // K chunks of 128 in a unit
 constexpr int AHEAD = 5;            // units of a share sent for L2 before the kernel may read: one round of the ring
@@ -178,6 +181,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
       if (C::PRE) {   // the ring's first round: weights, then the wait for the operand
         for (; i < min(nu, C::STAGES); ++i) { weights(i, rt, ku); next(rt, tt, ku); }
         pdl_wait();
+        fence_proxy_async_global();   // k_split_x's stores, read by bulk copies
         int rt2 = rt0, tt2 = tt0, ku2 = ku0;
         for (int j = 0; j < i; ++j) { operand(j, tt2, ku2); next(rt2, tt2, ku2); }
         if (i == C::STAGES) ph = 1;
@@ -248,7 +252,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
       const int k = ku * (UK * 128) + lane * 8;
       ku += ngrp;
       while (ku >= KU) ku -= KU;
-      return t < p.M && k < p.K ? __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.ldx + k))
+      return t < p.M && k < p.K ? __ldcg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.ldx + k))
                                 : make_uint4(0u, 0u, 0u, 0u);
     };
     uint4 buf[PD];
@@ -288,7 +292,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
       const bool mine = u == t0;                           // this share starts the tile and so finishes it
       const int c1 = mine ? sh.of(t1 - 1) : share;   // shares after this one that hold parts of it
       const int b = seg & 1;
-      const float bv = (p.bias && n < p.N) ? __ldg(p.bias + n) : 0.0f;
+      const float bv = (p.bias && n < p.N) ? __ldcg(p.bias + n) : 0.0f;
       // parts cb .. of tokens tb .. tb + TB - 1
       uint32_t w[CB][TB];
       auto peek = [&](int cb, int tb) {
@@ -405,7 +409,7 @@ __global__ void __launch_bounds__(256) k_split_x(const LinearParams p) {
   pdl_launch_dependents();
   constexpr int MT = NC / 2;
   const int kc = blockIdx.x, t = blockIdx.y * 16 + (threadIdx.x >> 4), g8 = threadIdx.x & 15, k = kc * 128 + g8 * 8;
-  const uint4 v = (t < p.M && k < p.K) ? __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.ldx + k))
+  const uint4 v = (t < p.M && k < p.K) ? __ldcg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.ldx + k))
                                        : make_uint4(0u, 0u, 0u, 0u);
   const int64_t blk = (int64_t)(t / MT) * p.KC + kc;
   if (t / MT < p.TT) split_item(v, p.xop + blk * (NC * 128), p.xsf + blk * SF_BLOCK, t % MT, MT, g8);

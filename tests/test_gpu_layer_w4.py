@@ -111,6 +111,8 @@ CASES = [
     (16, 2048, 128, 8, 384, 256, True, True, True),
     (16, 512, 512, 16, 128, 0, False, True, False),
     (1, 6144, 64, 8, 256, 256, True, False, True),
+    (2, 8192, 12, 3, 1024, 0, True, True, False),
+    (10, 3328, 20, 2, 1152, 640, False, True, True),
 ]
 
 
@@ -241,6 +243,51 @@ def test_captured_and_replayed_with_new_inputs(M):
             g.replay()
             st.synchronize()
             L.check(x, (out, ids, wts))
+
+
+def test_the_first_call_of_a_process_is_captured():
+    code = """
+import sys; sys.path.insert(0, 'tests')
+import torch
+import test_gpu_layer_w4 as t
+import prefill_moe_route_b200 as moe
+for M in (1, 2, 7, 12):
+    L = t.Layer(512, 16, 4, 256, 128)
+    ws = L.workspace()
+    x, out = L.x(M), torch.empty(M, 512, device='cuda', dtype=torch.bfloat16)
+    ids, wts = torch.empty(M, 4, device='cuda', dtype=torch.int32), torch.empty(M, 4, device='cuda')
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.moe_layer_w4(L.shape(M), L.weights, x, out, ids, wts, *ws)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    L.check(x, (out, ids, wts))
+print('child ok')
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "child ok" in r.stdout, r.stdout[-2000:] + r.stderr[-3000:]
+
+
+def test_a_chain_of_layers_on_one_buffer_pair():
+    """h goes back and forth through the layer; another stream's kernels run meanwhile."""
+    L = Layer(1024, 32, 4, 256, 128)
+    ws = L.workspace()
+    a, b = L.x(5), torch.empty(5, 1024, device=DEV, dtype=torch.bfloat16)
+    x = a.clone()
+    torch.cuda.synchronize()
+    other, busy = torch.cuda.Stream(), torch.randn(2048, 2048, device=DEV)
+    for i in range(20):
+        with torch.cuda.stream(other):
+            busy = busy @ busy * 1e-3
+        L.run(a, ws, out=b)
+        L.run(b, ws, out=a)
+    torch.cuda.synchronize()
+    for i in range(40):
+        x = L.run(x, ws)[0]
+        torch.cuda.synchronize()
+    assert torch.equal(a, x) and moe.moe_get_status(ws[0]) == (moe.MOE_OK, 0)
 
 
 def test_two_calls_at_once():

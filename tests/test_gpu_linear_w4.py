@@ -76,7 +76,7 @@ def _run(M, N, K, out_type, bias=None, mat=None, x=None, ws=None):
 
 SIZES = [(1, 1, 32), (1, 128, 128), (3, 127, 96), (1, 129, 160), (2, 300, 288), (8, 512, 512), (9, 256, 384),
          (16, 1000, 2912), (17, 64, 32), (31, 130, 416), (32, 512, 1024), (33, 129, 320), (64, 384, 512), (65, 257, 512),
-         (128, 128, 256), (200, 100, 2080), (1, 6144, 6144), (5, 4099, 2912), (40, 2000, 4096), (1, 20011, 512)]
+         (128, 128, 256), (200, 100, 2080), (1000, 300, 96), (3, 60, 40000), (40, 130, 32800), (2, 100003, 64), (1, 6144, 6144), (5, 4099, 2912), (40, 2000, 4096), (1, 20011, 512)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -232,6 +232,58 @@ def test_captured_and_replayed_with_new_inputs(M):
             g.replay()
             st.synchronize()
             _check(out, x, mat)
+
+
+def test_the_first_call_of_a_process_is_captured():
+    code = """
+import sys; sys.path.insert(0, 'tests')
+import torch
+import test_gpu_linear_w4 as t
+import prefill_moe_route_b200 as moe
+for M in (2, 40):
+    mat = t.Matrix(500, 640)
+    sh = moe.MoeLinearShape.of(M, 500, 640, out_type=moe.MOE_OUT_F32)
+    ws, n = t._workspace(sh)
+    x, out = t._x(M, 640), torch.empty(M, 500, device='cuda')
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.moe_linear_w4(sh, x, mat.packed, None, out, ws, n)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    t._check(out, x, mat)
+print('child ok')
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "child ok" in r.stdout, r.stdout[-2000:] + r.stderr[-3000:]
+
+
+def test_a_chain_rewrites_its_own_input():
+    """x is overwritten between the calls by kernels of the same stream, the library's and others."""
+    N = K = 1024
+    mat = Matrix(N, K, seed=3, lo=113, hi=116)
+    sh = moe.MoeLinearShape.of(6, N, K)
+    ws, n = _workspace(sh)
+    a, b = _x(6, K), torch.empty(6, N, device=DEV, dtype=torch.bfloat16)
+    want = a.clone()
+    for i in range(30):
+        moe.moe_linear_w4(sh, a, mat.packed, None, b, ws, n)
+        moe.moe_linear_w4(sh, b, mat.packed, None, a, ws, n)
+        if i % 3 == 0:
+            a.mul_(0.5)
+    got = a.clone()
+    x = want
+    for i in range(30):
+        for _ in range(2):
+            y = torch.empty_like(x)
+            torch.cuda.synchronize()
+            moe.moe_linear_w4(sh, x, mat.packed, None, y, ws, n)
+            torch.cuda.synchronize()
+            x = y
+        if i % 3 == 0:
+            x = x * 0.5
+    assert torch.equal(got, x)
 
 
 def test_two_calls_at_once():

@@ -34,7 +34,7 @@ def test_linear_refuses_shapes(bad):
 
 def test_linear_refuses_shapes_past_its_limits():
     n = ctypes.c_size_t(0)
-    for bad in (dict(M=(1 << 20) + 1), dict(N=(1 << 24) + 1, ldo=1 << 25), dict(N=1 << 24, ldo=1 << 24, K=1 << 20, ldx=1 << 20)):
+    for bad in (dict(M=(1 << 19) + 1), dict(N=(1 << 24) + 1, ldo=1 << 25), dict(N=1 << 24, ldo=1 << 24, K=1 << 20, ldx=1 << 20)):
         sh = _linear(**bad)
         assert moe.load().moe_linear_w4_workspace_size(ctypes.byref(sh), ctypes.byref(n)) == moe.MOE_ERR_UNSUPPORTED
 
@@ -57,6 +57,8 @@ def test_linear_refuses_pointers_before_any_launch():
     assert moe.moe_pack_w4(4104, 4096, 128, 128, 8192, stream=0, check=False) == moe.MOE_ERR_INVALID_ARG
     assert moe.moe_pack_w4(4096, 4096, 128, 128, 8208, stream=0, check=False) == moe.MOE_ERR_INVALID_ARG
     assert moe.moe_pack_w4(4096, 4096, 128, 100, 8192, stream=0, check=False) == moe.MOE_ERR_INVALID_ARG
+    assert moe.moe_pack_w4(4096, 1 << 20, 128, 128, 8192, stream=0, check=False) == moe.MOE_ERR_INVALID_ARG   # q overlaps
+    assert moe.moe_pack_w4(1 << 20, 8448, 128, 128, 8192, stream=0, check=False) == moe.MOE_ERR_INVALID_ARG   # scales do
     assert moe.moe_last_error()
 
 
