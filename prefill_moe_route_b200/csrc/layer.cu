@@ -140,17 +140,18 @@ __device__ __forceinline__ void split_chunk(const LayerParams& p, int kc) {
 template <bool NORM, bool HIGH>
 __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREADS, HIGH ? 3 : 4) k_layer_head(const LayerParams p) {
   constexpr int BATCH = 3;   // blocks in flight
-  {  // the router's rows start for L2 while the kernel before ends
-    const int e = blockIdx.x / HEAD_SLICES * 8 + (threadIdx.x >> 2 & 7);
-    if (e < p.E && (threadIdx.x & 3) == 0)
-      for (int b = blockIdx.x % HEAD_SLICES * 8 + (threadIdx.x >> 5); b < p.H / 32; b += 8 * HEAD_SLICES)
-        prefetch_l2_line(p.router_w + (int64_t)e * p.H + b * 32);
-  }
   __shared__ float sd[8][16][8], sq[8][16];
   __shared__ float cs[HEAD_SLICES][16 * 8 + 16];   // rank 0's: every slice's sums
   __shared__ uint64_t arrived;                     // rank 0's: their bytes
-  const int nlogit = (p.E + 7) / 8 * HEAD_SLICES;
+  const int M = p.M, H = p.H, E = p.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nlogit = (E + 7) / 8 * HEAD_SLICES;
   const bool logits = blockIdx.x < nlogit;         // the same for a whole cluster
+  const int eg = blockIdx.x / HEAD_SLICES, slice = blockIdx.x % HEAD_SLICES;
+  const int g = lane >> 2, kq = (lane & 3) * 8, nblk = H / 32;
+  const bool e_ok = eg * 8 + g < E, t0 = g < M, t1 = HIGH && g + 8 < M;
+  const uint16_t* wr = p.router_w + (int64_t)(e_ok ? eg * 8 + g : 0) * H + kq;
+  const uint16_t* x0 = p.x + (int64_t)(t0 ? g : 0) * p.ldx + kq;
+  const uint16_t* x1 = p.x + (int64_t)(t1 ? g + 8 : 0) * p.ldx + kq;
   if (logits) {
     if (threadIdx.x == 0) {
       mbar_init(&arrived, 1);
@@ -159,25 +160,21 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
     }
     __syncthreads();
     cluster_arrive_release();   // ready for the others' stores (waited for before they are made)
+    if (e_ok && (lane & 3) == 0)   // the router's rows start for L2 while the kernel before ends
+      for (int b = slice * 8 + warp; b < nblk; b += 8 * HEAD_SLICES) prefetch_l2_line(wr + b * 32);
   }
+  have(wr); have(x0); have(x1);
   pdl_wait();
   if (blockIdx.x + 1 == gridDim.x) {   // before any block of k_layer_experts can start
     if (threadIdx.x == 0) { p.sync[0] = 0; p.sync[1] = 0; __threadfence(); }
     __syncthreads();
   }
   pdl_launch_dependents();
-  const int M = p.M, H = p.H, E = p.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t deadline = globaltimer() + p.timeout_ns;
   if (!logits) {
     if (blockIdx.x - nlogit < H / 128) split_chunk(p, blockIdx.x - nlogit);
     return;
   }
-  const int eg = blockIdx.x / HEAD_SLICES, slice = blockIdx.x % HEAD_SLICES;
-  const int g = lane >> 2, kq = (lane & 3) * 8, nblk = H / 32;
-  const bool e_ok = eg * 8 + g < E, t0 = g < M, t1 = HIGH && g + 8 < M;
-  const uint16_t* wr = p.router_w + (int64_t)(e_ok ? eg * 8 + g : 0) * H + kq;
-  const uint16_t* x0 = p.x + (int64_t)(t0 ? g : 0) * p.ldx + kq;
-  const uint16_t* x1 = p.x + (int64_t)(t1 ? g + 8 : 0) * p.ldx + kq;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   float d[4] = {0.f, 0.f, 0.f, 0.f}, ss0 = 0.0f, ss1 = 0.0f;
 #pragma unroll 1

@@ -138,10 +138,11 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // Nothing above touches global memory.  With the operand made by k_split_x,
-  // which starts this kernel only after its own wait, everything but that
-  // operand is already there: only its reader waits.
-  if (!C::PRE) pdl_wait();
+  // Nothing above touches global memory but to send it for L2.  Each role works
+  // out what it can and then waits for the kernel before this one (0.4 us of the
+  // call otherwise).  With the operand made by k_split_x, which starts this kernel
+  // only after its own wait, everything but that operand is already there: only
+  // its reader waits.
   pdl_launch_dependents();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, S.tmem, 0);
   const uint64_t deadline = globaltimer() + p.timeout_ns;
@@ -178,6 +179,8 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
         bulk_load(bsf + s * C::SF_BYTES, p.xsf + blk * SF_BLOCK, nk * SF_BLOCK, &S.full[s]);
       };
       int rt = rt0, tt = tt0, ku = ku0, i = 0;
+      have(rt); have(tt); have(ku);
+      if (!C::PRE) pdl_wait();
       if (C::PRE) {   // the ring's first round: weights, then the wait for the operand
         for (; i < min(nu, C::STAGES); ++i) { weights(i, rt, ku); next(rt, tt, ku); }
         pdl_wait();
@@ -256,6 +259,8 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
                                 : make_uint4(0u, 0u, 0u, 0u);
     };
     uint4 buf[PD];
+    have(ku);
+    pdl_wait();
 #pragma unroll
     for (int d = 0; d < PD; ++d) buf[d] = load();
     bool ok = true;
@@ -283,6 +288,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
     constexpr int TB = 8;                   // tokens per step
     constexpr int CB = 4;                   // parts per batch: 32 loads in flight
     const int g0 = (warp - WARP_EPI0) / 4 * C::ET;   // this group's tokens of the tile
+    if (!C::PRE) pdl_wait();
     int seg = 0;
     bool ok = true;
     for (int u = u0; u < u1 && ok; ++seg) {

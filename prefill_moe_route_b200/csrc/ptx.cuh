@@ -180,6 +180,13 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// Has a value worked out by this point of the program (before a wait, say).
+template <typename T>
+__device__ __forceinline__ void have(const T& v) {
+  if constexpr (sizeof(T) == 8) asm volatile("" ::"l"(v) : "memory");
+  else asm volatile("" ::"r"(v) : "memory");
+}
+
 // ------------------------------------------------------------ PDL
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() {
