@@ -59,10 +59,10 @@ struct Cfg {                       // NC: operand columns, two per token
 };
 
 struct Smem {
-  uint64_t full[STAGES], empty[STAGES], accf[2], acce[2], tfull[TASKS], tempty[TASKS];
+  uint64_t full[STAGES], empty[STAGES], accf[2], acce[2], tfull[TASKS], tempty[TASKS], listed;
   uint32_t tmem;
   int abort_flag;
-  int task[TASKS];
+  int first_task, task[TASKS];
   float rstd[MAX_M];
   int ids[MAX_M * kMaxTopk];
   float wts[MAX_M * kMaxTopk];
@@ -341,6 +341,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     for (int s = 0; s < STAGES; ++s) { mbar_init(&S.full[s], 2); mbar_init(&S.empty[s], 1); }
     for (int b = 0; b < 2; ++b) { mbar_init(&S.accf[b], 1); mbar_init(&S.acce[b], epi_warps); }
     for (int t = 0; t < TASKS; ++t) { mbar_init(&S.tfull[t], 1); mbar_init(&S.tempty[t], 2 + epi_warps); }
+    mbar_init(&S.listed, 1 + epi_warps);
     S.abort_flag = 0;
     fence_mbar_init();
   }
@@ -359,11 +360,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
   // one, its end (pdl_wait) only by the reader of the operand columns.
   pdl_launch_dependents();
   const uint64_t deadline = globaltimer() + p.timeout_ns;
-  auto fail = [&](int site) {
-    *abort_flag = 1;
-    atomicOr(p.status, ST_TIMEOUT);
-    atomicCAS(p.status + 2, 0, (int)(0x80000000u | (9u << 24) | ((unsigned)site << 20) | (blockIdx.x & 0xFFFu)));
-  };
+  auto fail = [&](uint32_t site) { wait_ran_out(p.status, abort_flag, 9u << 24 | site << 20); };
   int ticket = 0;
   if (threadIdx.x == 0) ticket = atomicAdd(p.sync, 1);   // in flight while routing runs
   if (warp < M) {   // one token a warp: there are at least M warps
@@ -375,21 +372,24 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
       fail(10);
     fence_proxy_async_smem();   // the ring's next writers are asynchronous copies
   }
+  if (threadIdx.x == 0) S.first_task = ticket;
   __syncthreads();
   if (*abort_flag) {   // no routing, no work
     if (warp == 4) tmem_dealloc(S.tmem, C::TMEM_COLS);
     return;
   }
-  // the selected experts, ascending: prefix counts of the mask's words, a thread an expert
   const uint32_t mword = lane < kMaxE / 32 ? S.mask[lane] : 0u;
   int ndist;
   const int before = warp_exclusive_scan(__popc(mword), &ndist);
-  for (int i = warp; i < (E + 31) / 32; i += blockDim.x / 32) {
-    const uint32_t m = __shfl_sync(0xFFFFFFFFu, mword, i);
-    const int n = __shfl_sync(0xFFFFFFFFu, before, i) + __popc(m & ((1u << lane) - 1u));
-    if ((m >> lane) & 1u) S.dlist[n] = static_cast<uint16_t>(32 * i + lane);
+  if (warp >= 3) {   // the selected experts, ascending: for the weight stream and the sums
+    for (int i = warp - 3; i < (E + 31) / 32; i += 1 + epi_warps) {
+      const uint32_t m = __shfl_sync(0xFFFFFFFFu, mword, i);
+      const int n = __shfl_sync(0xFFFFFFFFu, before, i) + __popc(m & ((1u << lane) - 1u));
+      if ((m >> lane) & 1u) S.dlist[n] = static_cast<uint16_t>(32 * i + lane);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.listed);
   }
-  __syncthreads();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, S.tmem, 0);
   // GEMM1: tile i (a gate and an up tile; the shared expert's first) is chunk i
   // of GEMM2's K.  A unit is 128 K of a GEMM1 tile or two chunks of a GEMM2 tile.
@@ -414,13 +414,18 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     if (t < sh1.n + sh2.n) { const int c = sh1.n + sh2.n - 1 - t; return {2, c, CU, sh2.begin(c), sh2.begin(c + 1)}; }
     return {0, 0, 1, 0, 0};
   };
-  // The other roles take the tasks in the order that the weight stream drew them.
+  // The other roles take the tasks in the order that the weight stream drew
+  // them: the first as it is, the later ones from a ring.
   auto next_task = [&](int n, Task* k) -> bool {   // a whole warp
-    if (!mbar_wait(&S.tfull[n % TASKS], (n / TASKS) & 1, deadline, abort_flag)) { fail(1); return false; }
-    __syncwarp();
-    const int t = S.task[n % TASKS];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&S.tempty[n % TASKS]);
+    int t = S.first_task;
+    if (n > 0) {
+      const int r = (n - 1) % TASKS;
+      if (!mbar_wait(&S.tfull[r], ((n - 1) / TASKS) & 1, deadline, abort_flag)) { fail(1); return false; }
+      __syncwarp();
+      t = S.task[r];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.tempty[r]);
+    }
     *k = task_of(t);
     return k->gemm != 0;
   };
@@ -430,11 +435,15 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     if (lane == 0) {
       int st = 0;
       uint32_t ph = 0;
-      bool ok = true;
+      bool ok = mbar_wait(&S.listed, 0, deadline, abort_flag);
+      if (!ok) fail(11);
       for (int n = 0; ok; ++n) {
-        if (!mbar_wait(&S.tempty[n % TASKS], ((n / TASKS) & 1) ^ 1, deadline, abort_flag)) { fail(2); ok = false; break; }
-        S.task[n % TASKS] = ticket;
-        mbar_arrive(&S.tfull[n % TASKS]);
+        if (n > 0) {
+          const int r = (n - 1) % TASKS;
+          if (!mbar_wait(&S.tempty[r], (((n - 1) / TASKS) & 1) ^ 1, deadline, abort_flag)) { fail(2); ok = false; break; }
+          S.task[r] = ticket;
+          mbar_arrive(&S.tfull[r]);
+        }
         const Task k = task_of(ticket);
         if (!k.gemm) break;
         ticket = atomicAdd(p.sync, 1);
@@ -547,8 +556,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     uint32_t ph = 0;
     bool ok = true, mid_ready = false;
     Task k;
-    pdl_wait();                   // the tokens' columns are there
-    fence_proxy_async_global();   // k_layer_head's stores, read by bulk copies
+    pdl_wait();   // the tokens' columns are there: a kernel's end orders its stores before bulk copies too
     for (int n = 0; ok && (ok = next_task(n, &k)); ++n) {
       if (k.gemm == 2 && !mid_ready) {
         // every GEMM1 tile's warps have stored their piece of mid
@@ -592,7 +600,9 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     const int t0 = (warp - 4) / 4 * TG;            // this warp's tokens t0 .. t0 + TG - 1
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q) << 16) + t0;
     int seg = 0;
-    bool ok = true;
+    bool ok = mbar_wait(&S.listed, 0, deadline, abort_flag);
+    if (!ok) fail(11);
+    __syncwarp();
     Task k;
     // Adds the later shares' parts [share + 1, c1] of NV values per row, in K
     // order, to v; value i is token t0 + i % TG's.

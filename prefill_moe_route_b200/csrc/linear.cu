@@ -146,11 +146,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
   pdl_launch_dependents();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, S.tmem, 0);
   const uint64_t deadline = globaltimer() + p.timeout_ns;
-  auto fail = [&](int site) {
-    *abort_flag = 1;
-    atomicOr(p.status, ST_TIMEOUT);
-    atomicCAS(p.status + 2, 0, (int)(0x80000000u | (8u << 24) | ((unsigned)site << 20) | (blockIdx.x & 0xFFFu)));
-  };
+  auto fail = [&](uint32_t site) { wait_ran_out(p.status, abort_flag, 8u << 24 | site << 20); };
   auto drain = [&]() { const uint64_t until = globaltimer() + 2000000ull; while (globaltimer() < until) { } };
 
   if (warp == 0) {
@@ -184,7 +180,6 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
       if (C::PRE) {   // the ring's first round: weights, then the wait for the operand
         for (; i < min(nu, C::STAGES); ++i) { weights(i, rt, ku); next(rt, tt, ku); }
         pdl_wait();
-        fence_proxy_async_global();   // k_split_x's stores, read by bulk copies
         int rt2 = rt0, tt2 = tt0, ku2 = ku0;
         for (int j = 0; j < i; ++j) { operand(j, tt2, ku2); next(rt2, tt2, ku2); }
         if (i == C::STAGES) ph = 1;

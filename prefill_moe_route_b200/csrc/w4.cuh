@@ -82,13 +82,27 @@ __device__ __forceinline__ uint32_t tile_byte(uint32_t n, uint32_t k) {
 // Byte of row n's scale of group q (0..3) in a 512-byte scale block.
 __device__ __forceinline__ uint32_t sf_byte(uint32_t n, uint32_t q) { return 16u * (n & 31u) + 4u * (n >> 5) + q; }
 
-// a / b for 0 <= a < 2^31, b > 0, through the fp32 quotient (a few off at most):
-// integer divisions follow one another where a kernel works out its share.
+// A wait ran out: recorded in the status words, and the block's other roles are
+// told.  A function of its own keeps it out of the roles' code, which every call
+// fetches anew.
+static __device__ __noinline__ void wait_ran_out(int32_t* status, volatile int* abort_flag, uint32_t where) {
+  *abort_flag = 1;
+  atomicOr(status, ST_TIMEOUT);
+  atomicCAS(status + 2, 0, static_cast<int>(0x80000000u | where | (blockIdx.x & 0xFFFu)));
+}
+
+// a / b for 0 <= a < 2^31, b > 0 and a quotient below 2^21 (then the fp32 quotient
+// is at most 2 off): no branches, where integer divisions follow one another in
+// a single warp that works out its share.
 __device__ __forceinline__ int quick_div(int a, int b) {
   int q = __float2int_rz(__fdividef(static_cast<float>(a), static_cast<float>(b)));
   int r = a - q * b;
-  while (r < 0) { --q; r += b; }
-  while (r >= b) { ++q; r -= b; }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = r < 0 ? -1 : r >= b ? 1 : 0;
+    q += c;
+    r -= c * b;
+  }
   return q;
 }
 
