@@ -95,7 +95,7 @@ extern "C" {
 
 int moe_w4_packed_size(int32_t N, int32_t K, size_t* bytes) {
   if (!bytes || N < 1 || K < 32 || K % 32) return fail(MOE_ERR_INVALID_ARG, "moe_w4_packed_size: null pointer, N < 1 or K not a multiple of 32");
-  *bytes = (size_t)((N + 127) / 128) * ((K + 127) / 128) * 8704;
+  *bytes = (size_t)((N + 127ll) / 128) * ((K + 127ll) / 128) * 8704;
   return MOE_OK;
 }
 
@@ -103,7 +103,7 @@ int moe_pack_w4(const uint8_t* q, const uint8_t* scales, int32_t N, int32_t K, u
   size_t bytes = 0;
   if (!q || !scales || !packed) return fail(MOE_ERR_INVALID_ARG, "moe_pack_w4: null pointer argument");
   if (moe_w4_packed_size(N, K, &bytes) != MOE_OK) return fail(MOE_ERR_INVALID_ARG, "moe_pack_w4: N < 1 or K not a multiple of 32");
-  if ((int64_t)(bytes / 8704) * 128 > INT_MAX) return fail(MOE_ERR_UNSUPPORTED, "moe_pack_w4: matrix too large");
+  if (bytes / 8704 * 128 > INT_MAX) return fail(MOE_ERR_UNSUPPORTED, "moe_pack_w4: matrix too large");
   if (!aligned(q, 16) || !aligned(packed, 256)) return fail(MOE_ERR_INVALID_ARG, "moe_pack_w4: q needs 16-byte, packed 256-byte alignment");
   const uintptr_t p0 = reinterpret_cast<uintptr_t>(packed), p1 = p0 + bytes, q0 = reinterpret_cast<uintptr_t>(q),
                   s0 = reinterpret_cast<uintptr_t>(scales), n = N;

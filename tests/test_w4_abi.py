@@ -12,7 +12,8 @@ def _linear(**kw):
     return moe.MoeLinearShape(**d)
 
 
-@pytest.mark.parametrize("N,K,blocks", [(1, 32, 1), (128, 128, 1), (129, 128, 2), (128, 160, 2), (6144, 6144, 48 * 48)])
+@pytest.mark.parametrize("N,K,blocks", [(1, 32, 1), (128, 128, 1), (129, 128, 2), (128, 160, 2), (6144, 6144, 48 * 48),
+                                        (2**31 - 1, 32, 2**24), (1, 2**31 - 32, 2**24)])   # no 32-bit sums
 def test_packed_size_counts_blocks_of_128_by_128(N, K, blocks):
     assert moe.moe_w4_packed_size(N, K) == blocks * (8192 + 512)
 
