@@ -170,7 +170,6 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
     __syncthreads();
   }
   pdl_launch_dependents();
-  const uint64_t deadline = globaltimer() + p.timeout_ns;
   if (!logits) {
     if (blockIdx.x - nlogit < H / 128) split_chunk(p, blockIdx.x - nlogit);
     return;
@@ -240,7 +239,11 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
     st_async_cluster_f32(mapa_shared(smem_u32(&cs[slice][i]), 0), sum, mapa_shared(smem_u32(&arrived), 0));
   }
   if (slice != 0 || threadIdx.x >= 128) return;
-  for (uint32_t spins = 0; !mbar_try_wait_cluster(&arrived, 0);)   // bounded: k_layer_experts then finds nothing and says so
+  // The other slices wait for nothing more, so their sums do come; this block may
+  // not end before them.  The limit is far beyond that of k_layer_experts, which
+  // finds no sigmoids and says so.
+  const uint64_t deadline = globaltimer() + p.timeout_ns + 10000000000ull;
+  for (uint32_t spins = 0; !mbar_try_wait_cluster(&arrived, 0);)
     if ((++spins & 255u) == 0 && globaltimer() > deadline) return;
   const int t = threadIdx.x >> 3, e = eg * 8 + (threadIdx.x & 7);
   if (t >= M) return;
@@ -274,7 +277,7 @@ __device__ __forceinline__ bool pick(const LayerParams& p, int t, int* ids, floa
 #pragma unroll
       for (int i = 0; i < KPER; ++i) all &= w[i] != 0u;
       if (__all_sync(0xFFFFFFFFu, all)) break;
-      if ((++spins & 15u) == 0 && globaltimer() > deadline) return false;
+      if ((++spins & 15u) == 0 && __any_sync(0xFFFFFFFFu, globaltimer() > deadline)) return false;
     }
 #pragma unroll
     for (int i = 0; i < KPER; ++i) {
@@ -564,8 +567,8 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
         while (ld_acquire_gpu(p.sync + 1) < epi_warps * tiles1) {
           if ((++spins & 15u) == 0 && (*abort_flag || globaltimer() > deadline)) { fail(6); ok = false; break; }
         }
+        ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        __syncwarp();
         fence_proxy_async_global();
         mid_ready = true;
       }
@@ -619,6 +622,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     auto gather = [&](uint32_t* part, int share, int c1, auto& v, auto& w, auto nv_const) -> bool {   // w: the first batch
       constexpr int NV = decltype(nv_const)::value;
       uint32_t spins = 0;
+      bool in_time = true;
 #pragma unroll 1
       for (int cb = share + 1; cb <= c1;) {
         bool all = true;
@@ -641,11 +645,12 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
           if (cb > c1) break;
         } else if ((++spins & 15u) == 0 && (*abort_flag || globaltimer() > deadline)) {
           fail(8);
-          return false;
+          in_time = false;
+          break;
         }
         peek(part, cb, c1, w, nv_const);
       }
-      return true;
+      return __all_sync(0xFFFFFFFFu, in_time);   // lanes wait for different words: they give up together
     };
     // [share][group][value][row]
     uint32_t* part1 = p.part1 + t0 * 2 * 128 + row;
@@ -698,7 +703,8 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
                 if (c) wt[t] = S.wts[(t0 + t) * topk + c - 1];
               }
             }
-            if (!gather(part1, k.share, c1, v, pw, std::integral_constant<int, 2 * TG>())) { ok = false; break; }
+            ok = gather(part1, k.share, c1, v, pw, std::integral_constant<int, 2 * TG>());
+            if (!ok) break;
             float m[TG];
             int s[TG];
 #pragma unroll
@@ -744,7 +750,8 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
 #pragma unroll
             for (int t = 0; t < TG; ++t)
               r[t] = p.residual && live(t) ? __uint_as_float((uint32_t)__ldcg(p.x + (t0 + t) * p.ldx + h) << 16) : 0.0f;
-            if (!gather(part2, k.share, c1, v, pw, std::integral_constant<int, TG>())) { ok = false; break; }
+            ok = gather(part2, k.share, c1, v, pw, std::integral_constant<int, TG>());
+            if (!ok) break;
 #pragma unroll
             for (int t = 0; t < TG; ++t)
               if (live(t)) p.out[(t0 + t) * p.ldo + h] = bf16_bits(v[t] + r[t]);

@@ -354,6 +354,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
           }
           peek(cb, tb);
         }
+        ok = __all_sync(0xFFFFFFFFu, ok);   // lanes wait for different words: they give up together
         if (tb + TB < m) peek(share + 1, tb + TB);
         if (n < p.N && ok) {
 #pragma unroll
