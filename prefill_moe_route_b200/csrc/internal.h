@@ -198,7 +198,7 @@ struct LayerParams {
   uint32_t *part1, *part2;  // parts of cut tiles: [grid][gate, up of the tokens][128], [grid][tokens][128]; zero between calls
   uint32_t *sig, *rstd;     // sigmoids of the logits [M][E], the norm's factors [M], as parts (zero between calls)
   uint8_t *xop, *xsf;       // the tokens' operand blocks and scale blocks [H/128]
-  uint8_t *mop, *msf;       // mid's, one per GEMM1 tile
+  uint8_t *mop, *msf;       // mid's, one per GEMM1 tile (up to 4 tokens: inverted words, scales a word each)
   int64_t ldx, ldo;
   int M, H, I, S, E, topk;  // S: the shared expert's width, 0 without one
   int nc;                   // operand columns: 16 up to 8 tokens, else 32

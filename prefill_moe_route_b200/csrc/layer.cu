@@ -172,6 +172,13 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
   pdl_launch_dependents();
   if (!logits) {
     if (blockIdx.x - nlogit < H / 128) split_chunk(p, blockIdx.x - nlogit);
+    if (M <= GROUP) {   // mid's words are empty until they are made
+      const int64_t tiles = (int64_t)min(E, M * p.topk) * (p.I / 128) + p.S / 128, step = (int64_t)(gridDim.x - nlogit) * HEAD_THREADS;
+      const int64_t first = (int64_t)(blockIdx.x - nlogit) * HEAD_THREADS + threadIdx.x;
+      const uint4 empty = make_uint4(0u, 0u, 0u, 0u);
+      for (int64_t i = first; i < tiles * (16 * 128 / 16); i += step) __stcg(reinterpret_cast<uint4*>(p.mop) + i, empty);
+      for (int64_t i = first; i < tiles * (SF_BLOCK / 16); i += step) __stcg(reinterpret_cast<uint4*>(p.msf) + i, empty);
+    }
     return;
   }
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -322,7 +329,12 @@ __device__ __forceinline__ bool pick(const LayerParams& p, int t, int* ids, floa
 // NC: operand columns; TG: tokens a warp's group holds (1 and 2 for as many
 // tokens, else GROUP): the sums of a tile are spread over four warps a group, so
 // that the code is short and a tile's epilogue takes as long for 16 tokens as for 4.
-template <int NC, int TG>
+// WORDS: mid is handed over as inverted words (as the parts of sums are), which
+// two warps bring into the ring; else as bytes behind a counter, by bulk copies.
+// Words save the writer's fence, the counter's trip and the copy's start, but
+// every reader polls all it needs.  Words against counter (us): 1 token 17.0 /
+// 18.1, 4 small ones 10.0 / 10.5, 4 of H = 6144 27.3 / 27.3, 5 ragged 17.4 / 16.9.
+template <int NC, int TG, bool WORDS>
 __global__ void __launch_bounds__(TG == GROUP ? (NC == 32 ? MAX_THREADS : 384) : 256, TG == GROUP ? 1 : 2)
 k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant__ CUtensorMap tmW2,
                 const __grid_constant__ CUtensorMap tmS13, const __grid_constant__ CUtensorMap tmS2, const LayerParams p) {
@@ -343,7 +355,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) { mbar_init(&S.full[s], 2); mbar_init(&S.empty[s], 1); }
     for (int b = 0; b < 2; ++b) { mbar_init(&S.accf[b], 1); mbar_init(&S.acce[b], epi_warps); }
-    for (int t = 0; t < TASKS; ++t) { mbar_init(&S.tfull[t], 1); mbar_init(&S.tempty[t], 2 + epi_warps); }
+    for (int t = 0; t < TASKS; ++t) { mbar_init(&S.tfull[t], 1); mbar_init(&S.tempty[t], (WORDS ? 3 : 2) + epi_warps); }
     mbar_init(&S.listed, 1 + epi_warps);
     S.abort_flag = 0;
     fence_mbar_init();
@@ -431,6 +443,14 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     }
     *k = task_of(t);
     return k->gemm != 0;
+  };
+
+  auto choices_out = [&]() {   // a warp
+    if (blockIdx.x == 0)
+      for (int q = lane; q < M * topk; q += 32) {
+        if (p.ids_out) p.ids_out[q] = S.ids[q];
+        if (p.wts_out) p.wts_out[q] = S.wts[q];
+      }
   };
 
   if (warp == 0) {
@@ -553,14 +573,92 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     }
     if (*abort_flag) drain();
     __syncwarp();
-  } else if (warp == 2) {
+  } else if (warp == 2 || (WORDS && warp == 3)) {
     // ------------------------------------------------ operand columns: the tokens', then mid's
     int st = 0;
     uint32_t ph = 0;
-    bool ok = true, mid_ready = false;
+    bool ok = true, mid_ready = WORDS;
     Task k;
+    if (WORDS && warp == 3) choices_out();
     pdl_wait();   // the tokens' columns are there: a kernel's end orders its stores before bulk copies too
     for (int n = 0; ok && (ok = next_task(n, &k)); ++n) {
+      if constexpr (WORDS) {
+        const int nu = k.u1 - k.u0;
+        if (k.gemm == 2) {
+          // A unit's live columns, 16 bytes a lane and load, and their scales; units
+          // alternate between the two warps, each with two on their way (three and
+          // four: the same times).
+          constexpr int MX = TG, NLD = 4 * MX * 8 / 32, WD = 2;   // columns of a chunk / 2, loads of a unit
+          struct Unit { uint4 d[NLD], s; } w[WD];
+          const int half = warp - 2;
+          auto column = [&](int r) { const int c = r % (2 * MX); return c < MX ? c : MT - MX + c; };   // of row r of 4 MX
+          auto there = [&](int i, int r) { return 2 * i + r / (2 * MX) < tiles1 && (column(r) & (MT - 1)) < M; };
+          auto fetch = [&](Unit& v, int i) {
+#pragma unroll
+            for (int j = 0; j < NLD; ++j) {
+              const int r = (lane >> 3) + 4 * j;
+              v.d[j] = there(i, r) ? words_peek(reinterpret_cast<const uint32_t*>(p.mop + (2 * (int64_t)i + r / (2 * MX)) * C::B_TILE + column(r) * 128 + (lane & 7) * 16))
+                                   : make_uint4(1u, 1u, 1u, 1u);
+            }
+            v.s = 2 * i + (lane >> 4) < tiles1 && (lane & (MT - 1)) < M
+                      ? words_peek(reinterpret_cast<const uint32_t*>(p.msf + (2 * (int64_t)i + (lane >> 4)) * SF_BLOCK + (lane & 15) * 16))
+                      : make_uint4(1u, 1u, 1u, 1u);
+          };
+          auto whole = [&](const Unit& v) {
+            bool all = v.s.x && v.s.y && v.s.z && v.s.w;
+#pragma unroll
+            for (int j = 0; j < NLD; ++j) all &= v.d[j].x && v.d[j].y && v.d[j].z && v.d[j].w;
+            return __all_sync(0xFFFFFFFFu, all);
+          };
+          const int i0 = k.u0 - quick_div(k.u0, k.len) * k.len;
+          int id[WD];
+#pragma unroll
+          for (int d = 0; d < WD; ++d) {
+            id[d] = i0 + half + 2 * d;
+            while (id[d] >= k.len) id[d] -= k.len;
+            if (half + 2 * d < nu) fetch(w[d], id[d]);
+          }
+          for (int x0 = half; x0 < nu && ok; x0 += 2 * WD) {
+#pragma unroll
+            for (int d = 0; d < WD; ++d) {
+              const int x = x0 + 2 * d;
+              if (x >= nu) break;
+              uint32_t spins = 0;
+              while (ok && !whole(w[d])) {
+                if ((++spins & 15u) == 0 && __any_sync(0xFFFFFFFFu, *abort_flag || globaltimer() > deadline)) { fail(6); ok = false; }
+                else fetch(w[d], id[d]);
+              }
+              int s = st + x;
+              uint32_t sph = ph;
+              while (s >= STAGES) { s -= STAGES; sph ^= 1; }
+              if (!ok || !mbar_wait(&S.empty[s], sph ^ 1, deadline, abort_flag)) { fail(7); ok = false; break; }
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < NLD; ++j) {
+                const int r = (lane >> 3) + 4 * j;
+                if (there(id[d], r))
+                  *reinterpret_cast<uint4*>(bbuf + s * C::B_BYTES + r / (2 * MX) * C::B_TILE + column(r) * 128 + (lane & 7) * 16) =
+                      make_uint4(~w[d].d[j].x, ~w[d].d[j].y, ~w[d].d[j].z, ~w[d].d[j].w);
+              }
+              *reinterpret_cast<uint32_t*>(bsf + s * C::SF_BYTES + (lane >> 4) * SF_BLOCK + (lane & 15) * 16) =
+                  ~(__byte_perm(__byte_perm(w[d].s.x, w[d].s.y, 0x0040), __byte_perm(w[d].s.z, w[d].s.w, 0x0040), 0x5410));
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&S.full[s]);
+              if (x + 2 * WD < nu) {
+                id[d] += 2 * WD;
+                while (id[d] >= k.len) id[d] -= k.len;
+                fetch(w[d], id[d]);
+              }
+            }
+          }
+        }
+        if (k.gemm == 2 || warp == 3) {
+          st += nu;
+          while (st >= STAGES) { st -= STAGES; ph ^= 1; }
+          continue;
+        }
+      }
       if (k.gemm == 2 && !mid_ready) {
         // every GEMM1 tile's warps have stored their piece of mid
         uint32_t spins = 0;
@@ -592,11 +690,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     if (*abort_flag) drain();
     __syncwarp();
   } else if (warp == 3) {
-    if (blockIdx.x == 0)
-      for (int q = lane; q < M * topk; q += 32) {
-        if (p.ids_out) p.ids_out[q] = S.ids[q];
-        if (p.wts_out) p.wts_out[q] = S.wts[q];
-      }
+    choices_out();
   } else {
     // ------------------------------------------------ sums
     const int q = warp & 3, row = 32 * q + lane;   // TMEM lane quarter = warp % 4
@@ -724,6 +818,23 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
             for (int t = 0; t < TG; t += 2) {
               uint32_t hi, lo;
               split_f16x2(f16x2_of(m[t], m[TG > 1 ? t + 1 : t], 1.0f), hi, lo);
+              if constexpr (WORDS) {
+                // bytes of four rows (lanes) by four columns (hi and lo of two tokens),
+                // transposed: a lane stores four rows of one column as one word
+                uint32_t w = hi | lo << 16, o = __shfl_xor_sync(0xFFFFFFFFu, w, 2);
+                w = lane & 2 ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
+                o = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
+                w = lane & 1 ? __byte_perm(o, w, 0x7351) : __byte_perm(w, o, 0x6240);
+                const int tok = t0 + t + (lane & 1), col = (lane & 2 ? MT : 0) + tok;
+                if (!(p.test_withhold && tile == 0) && (TG > 1 || !(lane & 1)) && tok < M) {
+                  word_put(reinterpret_cast<uint32_t*>(dst + tile_byte(col, row & ~3)), w);
+                  if (lane < 4)   // this block of 32 rows' scale, a word of its own
+                    word_put(reinterpret_cast<uint32_t*>(sf + 16 * col) + q,
+                             static_cast<uint32_t>(lane & 2 ? split_code_lo(lane & 1 ? s[TG > 1 ? t + 1 : t] : s[t])
+                                                            : split_code_hi(lane & 1 ? s[TG > 1 ? t + 1 : t] : s[t])));
+                }
+                continue;
+              }
 #pragma unroll
               for (int o = 0; o < min(2, TG); ++o)
                 if (live(t + o)) {
@@ -735,8 +846,10 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
                   }
                 }
             }
-            __syncwarp();   // the release below covers the warp's stores
-            if (lane == 0 && !(p.test_withhold && tile == 0)) red_release_gpu(p.sync + 1, 1);
+            if constexpr (!WORDS) {
+              __syncwarp();   // the release below covers the warp's stores
+              if (lane == 0 && !(p.test_withhold && tile == 0)) red_release_gpu(p.sync + 1, 1);
+            }
           }
         } else {
           if (!mine) {
@@ -784,14 +897,14 @@ static cudaLaunchConfig_t config(int grid, int threads, int smem, cudaStream_t s
   return cfg;
 }
 
-template <int NC, int TG>
+template <int NC, int TG, bool WORDS>
 static cudaError_t launch_experts(const CUtensorMap* m, const LayerParams& p, int grid, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = set_up_kernel(k_layer_experts<NC, TG>, smem_bytes<NC>(), &ready);
+  const cudaError_t e = set_up_kernel(k_layer_experts<NC, TG, WORDS>, smem_bytes<NC>(), &ready);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = config(grid, 128 + 128 * ((p.M + TG - 1) / TG), smem_bytes<NC>(), st, &attr);
-  return cudaLaunchKernelEx(&cfg, k_layer_experts<NC, TG>, m[0], m[1], m[2], m[3], p);
+  return cudaLaunchKernelEx(&cfg, k_layer_experts<NC, TG, WORDS>, m[0], m[1], m[2], m[3], p);
 }
 
 template <bool NORM, bool HIGH>
@@ -812,10 +925,11 @@ cudaError_t launch_layer_w4(const CUtensorMap* maps, const LayerParams& p, int s
   const cudaError_t e = p.norm_w ? (p.M > 8 ? launch_head<true, true>(p, st) : launch_head<true, false>(p, st))
                                  : (p.M > 8 ? launch_head<false, true>(p, st) : launch_head<false, false>(p, st));
   if (e != cudaSuccess) return e;
-  if (p.M == 1) return launch_experts<16, 1>(maps, p, sms, st);
-  if (p.M == 2) return launch_experts<16, 2>(maps, p, sms, st);
-  if (p.M <= 8) return launch_experts<16, GROUP>(maps, p, sms, st);
-  return launch_experts<32, GROUP>(maps, p, sms, st);
+  if (p.M == 1) return launch_experts<16, 1, true>(maps, p, sms, st);
+  if (p.M == 2) return launch_experts<16, 2, true>(maps, p, sms, st);
+  if (p.M <= GROUP) return launch_experts<16, GROUP, true>(maps, p, sms, st);
+  if (p.M <= 8) return launch_experts<16, GROUP, false>(maps, p, sms, st);
+  return launch_experts<32, GROUP, false>(maps, p, sms, st);
 }
 
 }  // namespace moe

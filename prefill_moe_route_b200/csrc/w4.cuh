@@ -120,6 +120,14 @@ __device__ __forceinline__ uint32_t part_peek(const uint32_t* p) {
   return v;
 }
 __device__ __forceinline__ float part_value(uint32_t word) { return __uint_as_float(~word); }
+__device__ __forceinline__ void word_put(uint32_t* p, uint32_t v) {   // v: not all ones
+  asm volatile("st.relaxed.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(~v) : "memory");
+}
+__device__ __forceinline__ uint4 words_peek(const uint32_t* p) {   // still inverted
+  uint4 v;
+  asm volatile("ld.relaxed.gpu.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
 
 // Once per device and kernel: its dynamic shared memory, and the split of the
 // SM's memory towards shared memory, without which a small kernel cannot run
