@@ -26,7 +26,6 @@ using namespace w4;
 
 constexpr int WARP_SPLIT0 = 2;
 constexpr int UK = 2;               // K chunks of 128 in a unit
-constexpr int AHEAD = 5;            // units of a share sent for L2 before the kernel may read: one round of the ring
 constexpr int SF_SLOTS = 4;         // TMEM scale slots: per chunk 4 columns of weight scales + 4 of token scales
 
 // NC: operand columns, two per token.  SW: warps that split the tokens' K chunks
@@ -46,6 +45,11 @@ struct Cfg {
   static constexpr int A_BYTES = UK * A_TILE, B_BYTES = UK * B_TILE, SF_BYTES = UK * SF_BLOCK;
   static constexpr int STAGE = A_BYTES + B_BYTES + 2 * SF_BYTES;   // weights, tokens, their scales
   static constexpr int STAGES = NC >= 128 ? 3 : NC >= 64 ? 4 : 5;
+  // units of a share sent for L2 before the kernel may read: a round of the ring (more
+  // is slower: 8, 12, 16 units of 1 x 6144 x 6144), and where k_split_x comes first
+  // and leaves the time, more (us, 8 / 5 / none: 16 x 6144 x 6144 8.9 / 9.2 / 9.8,
+  // 32 x 6144 x 12288 13.3 / 13.2 / 13.5)
+  static constexpr int AHEAD = NC == 32 ? 8 : 5;
   static constexpr int TMEM_COLS = NC >= 128 ? 512 : 256;
   static constexpr int SF_COL0 = 2 * NC;
 };
@@ -87,8 +91,8 @@ __device__ __forceinline__ void split_item(const uint4& u, uint8_t* tile, uint8_
 // A share's first units start for L2 while the kernel before this call ends (a
 // prefetch only: what that kernel writes stays what is read).  1 x 6144 x 6144:
 // 7.4 us without, 6.8 with.
-__device__ __forceinline__ void prefetch_weights(const LinearParams& p, int share) {
-  const int u0 = p.shares.begin(share), n = min(p.shares.begin(share + 1) - u0, AHEAD);
+__device__ __forceinline__ void prefetch_weights(const LinearParams& p, int share, int ahead) {
+  const int u0 = p.shares.begin(share), n = min(p.shares.begin(share + 1) - u0, ahead);
   int tile = u0 / p.KU, ku = u0 - tile * p.KU;
   for (int i = 0; i < n; ++i) {
     const int64_t blk = (int64_t)(tile / p.TT) * p.KC + ku * UK;
@@ -132,7 +136,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
   }
   if (threadIdx.x == 32) {
     tma_prefetch_desc(&tmW);
-    if (!C::PRE) prefetch_weights(p, share);
+    prefetch_weights(p, share, C::AHEAD);
   }
   if (warp == WARP_EPI0) { tmem_alloc(&S.tmem, C::TMEM_COLS); tmem_relinquish(); }
   tc_fence_before();
@@ -140,9 +144,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
   tc_fence_after();
   // Nothing above touches global memory but to send it for L2.  Each role works
   // out what it can and then waits for the kernel before this one (0.4 us of the
-  // call otherwise).  With the operand made by k_split_x, which starts this kernel
-  // only after its own wait, everything but that operand is already there: only
-  // its reader waits.
+  // call otherwise); k_split_x waits for the kernel before the call first.
   pdl_launch_dependents();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, S.tmem, 0);
   const uint64_t deadline = globaltimer() + p.timeout_ns;
@@ -155,7 +157,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
       int st = 0;
       uint32_t ph = 0;
       bool ok = true;
-      const int tile0 = u0 / KU, ku0 = u0 - tile0 * KU, rt0 = tile0 / TT, tt0 = tile0 - rt0 * TT;
+      const int tile0 = u0 / KU;
       auto next = [&](int& rt, int& tt, int& ku) {
         if (++ku == KU) { ku = 0; if (++tt == TT) { tt = 0; ++rt; } }
       };
@@ -174,18 +176,10 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
         bulk_load(bbuf + s * C::B_BYTES, p.xop + blk * C::B_TILE, nk * C::B_TILE, &S.full[s]);
         bulk_load(bsf + s * C::SF_BYTES, p.xsf + blk * SF_BLOCK, nk * SF_BLOCK, &S.full[s]);
       };
-      int rt = rt0, tt = tt0, ku = ku0, i = 0;
+      int rt = tile0 / TT, tt = tile0 - rt * TT, ku = u0 - tile0 * KU;
       have(rt); have(tt); have(ku);
-      if (!C::PRE) pdl_wait();
-      if (C::PRE) {   // the ring's first round: weights, then the wait for the operand
-        for (; i < min(nu, C::STAGES); ++i) { weights(i, rt, ku); next(rt, tt, ku); }
-        pdl_wait();
-        int rt2 = rt0, tt2 = tt0, ku2 = ku0;
-        for (int j = 0; j < i; ++j) { operand(j, tt2, ku2); next(rt2, tt2, ku2); }
-        if (i == C::STAGES) ph = 1;
-        else st = i;
-      }
-      for (; i < nu; ++i) {
+      pdl_wait();
+      for (int i = 0; i < nu; ++i) {
         if (!mbar_wait(&S.empty[st], ph ^ 1, deadline, abort_flag)) { fail(1); ok = false; break; }
         weights(st, rt, ku);
         if (C::PRE) operand(st, tt, ku);
@@ -283,7 +277,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
     constexpr int TB = 8;                   // tokens per step
     constexpr int CB = 4;                   // parts per batch: 32 loads in flight
     const int g0 = (warp - WARP_EPI0) / 4 * C::ET;   // this group's tokens of the tile
-    if (!C::PRE) pdl_wait();
+    pdl_wait();
     int seg = 0;
     bool ok = true;
     for (int u = u0; u < u1 && ok; ++seg) {
@@ -407,8 +401,8 @@ __global__ void __launch_bounds__(256) k_pack_w4(const uint8_t* __restrict__ q, 
 // one token, 16 tokens a CTA.
 template <int NC>
 __global__ void __launch_bounds__(256) k_split_x(const LinearParams p) {
+  pdl_launch_dependents();   // k_linear_w4 sets up, sends weights for L2 and waits for this kernel's end
   pdl_wait();
-  pdl_launch_dependents();
   constexpr int MT = NC / 2;
   const int kc = blockIdx.x, t = blockIdx.y * 16 + (threadIdx.x >> 4), g8 = threadIdx.x & 15, k = kc * 128 + g8 * 8;
   const uint4 v = (t < p.M && k < p.K) ? __ldcg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.ldx + k))
