@@ -37,10 +37,13 @@ struct Cfg {
   static constexpr int MT = NC / 2;
   static constexpr bool PRE = SW == 0;
   static constexpr int WARP_EPI0 = WARP_SPLIT0 + (PRE ? 2 : SW);   // the two are idle: TMEM quarters
-  // the sums of 16 tokens a group of four warps: one after another their trips
-  // through L2 would add up
-  static constexpr int EG = MT > 16 ? MT / 16 : 1, ET = MT / EG;
+  // the sums of 8 or 16 tokens a group of four warps: one after another their trips
+  // through L2 would add up (16 x 6144 x 6144, one group / two: 8.9 / 8.2 us)
+  static constexpr int EG = MT >= 64 ? 4 : MT >= 16 ? 2 : 1, ET = MT / EG;
   static constexpr int THREADS = (WARP_EPI0 + 4 * EG) * 32;
+  // Registers for blocks of k_split_x beside this one: the next call's start early
+  // (64 x 6144 x 6144, at most 96 registers / 80: 13.3 / 12.4 us).
+  static constexpr int BOUND = THREADS > 512 ? 768 : THREADS;
   static constexpr int B_TILE = NC * 128;
   static constexpr int A_BYTES = UK * A_TILE, B_BYTES = UK * B_TILE, SF_BYTES = UK * SF_BLOCK;
   static constexpr int STAGE = A_BYTES + B_BYTES + 2 * SF_BYTES;   // weights, tokens, their scales
@@ -104,7 +107,7 @@ __device__ __forceinline__ void prefetch_weights(const LinearParams& p, int shar
 }
 
 template <int NC, int SW>
-__global__ void __launch_bounds__(Cfg<NC, SW>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<NC, SW>::BOUND, 1)
 k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
   using C = Cfg<NC, SW>;
   constexpr int MT = C::MT, WARP_EPI0 = C::WARP_EPI0;
