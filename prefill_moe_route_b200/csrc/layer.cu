@@ -333,9 +333,11 @@ __device__ __forceinline__ bool pick(const LayerParams& p, int t, int* ids, floa
 // two warps bring into the ring; else as bytes behind a counter, by bulk copies.
 // Words save the writer's fence, the counter's trip and the copy's start, but
 // every reader polls all it needs.  Words against counter (us): 1 token 17.0 /
-// 18.1, 4 small ones 10.0 / 10.5, 4 of H = 6144 27.3 / 27.3, 5 ragged 17.4 / 16.9.
+// 18.1, 4 small ones 10.0 / 10.5, 4 of H = 6144 26.5 / 27.3, 5 ragged 17.4 / 16.9.
+// At most 128 registers there: two blocks of the next call's k_layer_head start
+// beside this one (with 142 registers one; 4 tokens of H = 6144 27.4 us).
 template <int NC, int TG, bool WORDS>
-__global__ void __launch_bounds__(TG == GROUP ? (NC == 32 ? MAX_THREADS : 384) : 256, TG == GROUP ? 1 : 2)
+__global__ void __launch_bounds__(WORDS ? 256 : NC == 32 ? MAX_THREADS : 384, WORDS ? 2 : 1)
 k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant__ CUtensorMap tmW2,
                 const __grid_constant__ CUtensorMap tmS13, const __grid_constant__ CUtensorMap tmS2, const LayerParams p) {
   using C = Cfg<NC>;
