@@ -37,13 +37,11 @@ struct Cfg {
   static constexpr int MT = NC / 2;
   static constexpr bool PRE = SW == 0;
   static constexpr int WARP_EPI0 = WARP_SPLIT0 + (PRE ? 2 : SW);   // the two are idle: TMEM quarters
-  // the sums of 8 or 16 tokens a group of four warps: one after another their trips
-  // through L2 would add up (16 x 6144 x 6144, one group / two: 8.9 / 8.2 us)
-  static constexpr int EG = MT >= 64 ? 4 : MT >= 16 ? 2 : 1, ET = MT / EG;
+  // the sums of 8 tokens (of a tile of 64: 16) a group of four warps: one after
+  // another their trips through L2 would add up (16 x 6144 x 6144, one group / two:
+  // 8.9 / 8.2 us; 32 x 6144 x 6144, two / four: 9.7 / 9.3)
+  static constexpr int EG = MT >= 32 ? 4 : MT / 8, ET = MT / EG;
   static constexpr int THREADS = (WARP_EPI0 + 4 * EG) * 32;
-  // Registers for blocks of k_split_x beside this one: the next call's start early
-  // (64 x 6144 x 6144, at most 96 registers / 80: 13.3 / 12.4 us).
-  static constexpr int BOUND = THREADS > 512 ? 768 : THREADS;
   static constexpr int B_TILE = NC * 128;
   static constexpr int A_BYTES = UK * A_TILE, B_BYTES = UK * B_TILE, SF_BYTES = UK * SF_BLOCK;
   static constexpr int STAGE = A_BYTES + B_BYTES + 2 * SF_BYTES;   // weights, tokens, their scales
@@ -107,7 +105,7 @@ __device__ __forceinline__ void prefetch_weights(const LinearParams& p, int shar
 }
 
 template <int NC, int SW>
-__global__ void __launch_bounds__(Cfg<NC, SW>::BOUND, 1)
+__global__ void __launch_bounds__(Cfg<NC, SW>::THREADS, 1)
 k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
   using C = Cfg<NC, SW>;
   constexpr int MT = C::MT, WARP_EPI0 = C::WARP_EPI0;
@@ -278,7 +276,11 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
     const int q = warp & 3, row = 32 * q + lane;   // TMEM lane quarter = warp % 4
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q) << 16);
     constexpr int TB = 8;                   // tokens per step
-    constexpr int CB = 4;                   // parts per batch: 32 loads in flight
+    // Parts looked for at once.  Two keep the 640 threads of the larger tiles near 64
+    // registers, and blocks of the next call's k_split_x start beside this one (us,
+    // 4 / 2: 32 x 6144 x 12288 14.4 / 12.9, 64 x 6144 x 6144 13.3 / 12.1; 16 x 6144 x
+    // 6144 8.2 / 8.3).
+    constexpr int CB = MT >= 32 ? 2 : 4;
     const int g0 = (warp - WARP_EPI0) / 4 * C::ET;   // this group's tokens of the tile
     pdl_wait();
     int seg = 0;
