@@ -30,8 +30,8 @@ constexpr int SF_SLOTS = 4;         // TMEM scale slots: per chunk 4 columns of 
 
 // NC: operand columns, two per token.  SW: warps that split the tokens' K chunks
 // in the kernel; 0: k_split_x has done it before.  Measured (us, N = K = 6144, 8
-// split warps / 16 / before): 4 tokens 7.7 / 8.1 / 9.4, 8 tokens 9.1 / 8.3 / 9.6,
-// 16 tokens 11.5 / 10.9 / 10.6 (N = 12288: 17.4 / 15.8 / 13.5).
+// split warps / 16 / before): 4 tokens 6.9 / 7.4 / 8.1, 8 tokens 7.8 / 7.8 / 8.3 (7 x
+// 4099 x 2912: 5.2 / 5.6 / 6.1), 16 tokens - / 9.2 / 8.2 (N = 12288: - / 13.4 / 11.4).
 template <int NC, int SW>
 struct Cfg {
   static constexpr int MT = NC / 2;
@@ -123,11 +123,11 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
   const int KU = p.KU, TT = p.TT;
   const Shares sh = p.shares;
   const int u0 = sh.begin(share), u1 = sh.begin(share + 1), nu = u1 - u0;
-  // warps that share one unit's split, one for a token; the groups of them, two or
-  // four, must not outnumber the stages (one two rounds ahead of the MMA would
-  // read a slot's old phase)
+  // warps that share one unit's split, one for a token; the groups of them, four at
+  // most, must not outnumber the stages (one two rounds ahead of the MMA would read
+  // a slot's old phase)
   const int gw = p.M <= 2 ? 2 : p.M <= 4 ? 4 : 8;
-  static_assert(C::PRE || (SW <= 8 ? SW / 2 : SW / 8) <= C::STAGES, "ring depth");
+  static_assert(C::PRE || SW / 2 <= C::STAGES, "ring depth");
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) { mbar_init(&S.full[s], C::PRE ? 1 : 1 + gw); mbar_init(&S.empty[s], 1); }
@@ -239,7 +239,8 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
     // A lane owns 8 of the unit's 256 K, a warp of the unit's gw one token (all fit one token tile).
     const int sw = warp - WARP_SPLIT0, grp = sw / gw, ngrp = SW / gw, t = sw % gw;
     const int kk = lane >> 4, g8 = lane & 15;
-    constexpr int PD = 4;   // units' loads in flight: a unit is consumed faster than L2 answers
+    constexpr int PD = 2;   // a warp's loads in flight (more is more cold code; us, 2 / 4: 7 x 4099 x 2912 5.0 / 5.2,
+                            // 1 x 512 x 512 2.7 / 2.8, 8 x 12288 x 6144 11.6 / 11.4)
     int ku = (u0 + grp) % KU;
     auto load = [&]() -> uint4 {   // and on to this group's next unit
       const int k = ku * (UK * 128) + lane * 8;
@@ -448,7 +449,7 @@ static cudaError_t launch(const CUtensorMap& w, const LinearParams& p, int grid,
 
 cudaError_t launch_linear_w4(const CUtensorMap& w, const LinearParams& p, int nc, int grid, cudaStream_t st) {
   switch (nc) {
-    case 16: return p.M <= 4 ? linear::launch<16, 8>(w, p, grid, st) : linear::launch<16, 16>(w, p, grid, st);
+    case 16: return linear::launch<16, 8>(w, p, grid, st);
     case 32: return linear::launch<32, 0>(w, p, grid, st);
     case 64: return linear::launch<64, 0>(w, p, grid, st);
     default: return linear::launch<128, 0>(w, p, grid, st);
