@@ -18,11 +18,14 @@
 // between router, routing, GEMM1, mid and GEMM2.  H = 6144, E = 256, top-8: 16
 // tokens with I = 512 take 83 us (66 experts, 4.1 TB/s: GEMM1 streams at 5.7, GEMM2 at
 // 5.2, 8 us lie between), 4 tokens with I = 256 26.4 us (26 experts, 2.7 TB/s), 1
-// token 16.9 us (1.5 TB/s).  Both products are cut into shares of equal bytes (as in linear.cu, parts of a cut tile meet in the share
-// that starts it, in K order).  Shares are tasks that the CTAs draw from one
-// counter, all of GEMM1 before all of GEMM2, and a task waits for earlier ones
-// only, so the kernel ends however many of its CTAs run at once.  A CTA's
-// weight stream runs ahead into its GEMM2 task while mid is still on its way.
+// token 16.9 us (1.5 TB/s).  Both products are cut into shares of equal bytes (as in
+// linear.cu, parts of a cut tile meet in the share that starts it, in K order), one
+// a CTA: twice as many, smaller ones cost more in parts than they balance (16 tokens
+// 85.0 us, 4 tokens 28.6).  Shares are tasks that the CTAs draw from one counter,
+// all of GEMM1 before all of GEMM2, and a task waits for earlier ones only, so the
+// kernel ends however many of its CTAs run at once.  A CTA's weight stream runs
+// ahead into its GEMM2 task while mid is still on its way, a ring's length (sending
+// more for L2 then: 16 tokens 85.0 us, it stands before the operands).
 #include <algorithm>
 #include <type_traits>
 
