@@ -712,7 +712,9 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     // Adds the later shares' parts [share + 1, c1] of NV values per row, in K
     // order, to v; value i is token t0 + i % TG's.
     auto live = [&](int i) { return t0 + (i & (TG - 1)) < M; };
-    constexpr int CB = 16 / TG;                    // parts in flight
+    // Parts in flight: about what a tile has; more is more code that runs cold (16 / TG
+    // of them and these, us: 16 tokens 83.1 / 82.5, 1 token 17.0 / 16.8)
+    constexpr int CB = NC == 32 ? 2 : TG == GROUP ? 3 : 8;
     auto peek = [&](const uint32_t* part, int cb, int c1, auto& w, auto nv_const) {   // parts cb .. c1, CB at most
       constexpr int NV = decltype(nv_const)::value;
 #pragma unroll
@@ -764,7 +766,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
         const int c1 = mine ? (k.gemm == 1 ? sh1 : sh2).of(te - 1) : k.share;
         const int b = seg & 1;
         // most parts are there before this share's own sum is: look for them first
-        uint32_t pw[16 / TG][2 * TG];
+        uint32_t pw[CB][2 * TG];
         if (k.gemm == 1) peek(part1, k.share + 1, c1, pw, std::integral_constant<int, 2 * TG>());
         else peek(part2, k.share + 1, c1, pw, std::integral_constant<int, TG>());
         if (!mbar_wait(&S.accf[b], (seg >> 1) & 1, deadline, abort_flag)) { fail(9); ok = false; break; }
