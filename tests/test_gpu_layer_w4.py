@@ -194,7 +194,7 @@ def test_zero_tokens_and_wide_ranges():
     L.check(x, L.run(x, L.workspace()))
 
 
-@pytest.mark.parametrize("M", [2, 8, 16])
+@pytest.mark.parametrize("M", [1, 2, 4, 8, 16])
 def test_a_token_that_is_not_finite_is_nan_alone(M):
     L = Layer(512, 16, 4, 256, 128)
     ws = L.workspace()
@@ -221,7 +221,7 @@ def test_optional_outputs_and_absent_parts():
     assert torch.equal(out, want[0])
 
 
-@pytest.mark.parametrize("M", [1, 5, 16])
+@pytest.mark.parametrize("M", [1, 4, 5, 16])
 def test_captured_and_replayed_with_new_inputs(M):
     L = Layer(1024, 64, 6, 256, 256)
     ws = L.workspace()
@@ -390,14 +390,15 @@ def test_refusals_on_the_device():
     assert rc() == moe.MOE_OK
 
 
-def test_a_flag_that_never_comes_ends_in_a_status():
+@pytest.mark.parametrize("M", [1, 4, 8, 16])
+def test_a_flag_that_never_comes_ends_in_a_status(M):
     code = """
 import sys; sys.path.insert(0, 'tests')
 import test_gpu_layer_w4 as t
 import prefill_moe_route_b200 as moe
 L = t.Layer(1024, 16, 4, 256, 128)
 ws = L.workspace()
-x = L.x(4)
+x = L.x(int(sys.argv[1]))
 L.run(x, ws)
 rc, st = moe.moe_get_status(ws[0])
 assert rc == moe.MOE_ERR_DEVICE_TIMEOUT and st == 1, (rc, st)
@@ -407,5 +408,5 @@ assert moe.moe_get_status(ws[0]) == (moe.MOE_OK, 0)
 print('child ok')
 """
     env = dict(os.environ, MOE_TEST_WITHHOLD_FLAG="1", MOE_WAIT_TIMEOUT_MS="20")
-    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, env=env, capture_output=True, text=True, timeout=300)
+    r = subprocess.run([sys.executable, "-c", code, str(M)], cwd=ROOT, env=env, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "child ok" in r.stdout, r.stdout[-2000:] + r.stderr[-3000:]

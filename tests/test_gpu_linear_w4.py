@@ -321,7 +321,8 @@ def test_refusals_on_the_device():
     assert moe.moe_linear_w4(sh, x.data_ptr() + 2, mat.packed, None, out, ws, n, check=False) == moe.MOE_ERR_INVALID_ARG
 
 
-def test_a_part_that_never_comes_ends_in_a_status():
+@pytest.mark.parametrize("M", [2, 8, 16, 32, 70])
+def test_a_part_that_never_comes_ends_in_a_status(M):
     """A withheld part of a sum: the waits on it run out, the call ends, the
     status says so; after a zero-fill the workspace serves again."""
     code = """
@@ -330,16 +331,17 @@ import torch
 import test_gpu_linear_w4 as t
 import prefill_moe_route_b200 as moe
 mat = t.Matrix(1024, 4096)
-sh = moe.MoeLinearShape.of(2, 1024, 4096, out_type=moe.MOE_OUT_F32)
+M = int(sys.argv[1])
+sh = moe.MoeLinearShape.of(M, 1024, 4096, out_type=moe.MOE_OUT_F32)
 ws, n = t._workspace(sh)
-out = torch.empty(2, 1024, device='cuda')
-moe.moe_linear_w4(sh, t._x(2, 4096), mat.packed, None, out, ws, n)
+out = torch.empty(M, 1024, device='cuda')
+moe.moe_linear_w4(sh, t._x(M, 4096), mat.packed, None, out, ws, n)
 rc, st = moe.moe_get_status(ws)
 assert rc == moe.MOE_ERR_DEVICE_TIMEOUT and st == 1, (rc, st)
 moe.moe_workspace_init(ws, n)
-t._run(2, 1024, 4096, moe.MOE_OUT_F32, mat=mat, ws=(ws, n))
+t._run(M, 1024, 4096, moe.MOE_OUT_F32, mat=mat, ws=(ws, n))
 print('child ok')
 """
     env = dict(os.environ, MOE_TEST_WITHHOLD_FLAG="1", MOE_WAIT_TIMEOUT_MS="20")
-    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, env=env, capture_output=True, text=True, timeout=300)
+    r = subprocess.run([sys.executable, "-c", code, str(M)], cwd=ROOT, env=env, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "child ok" in r.stdout, r.stdout[-2000:] + r.stderr[-3000:]
