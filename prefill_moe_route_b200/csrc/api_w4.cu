@@ -34,7 +34,14 @@ static int linear_plan(const moe_linear_shape_t& s, int sms, LinearPlan* p) {
   p->KC = (s.K + 127) / 128;
   p->KU = (p->KC + 1) / 2;                 // a unit is two chunks
   if ((int64_t)p->RT * p->KC * 128 > INT_MAX) return MOE_ERR_UNSUPPORTED;   // rows of the packed tensor map
-  p->nc = s.M <= 8 ? 16 : s.M <= 16 ? 32 : s.M <= 32 ? 64 : 128;
+  // Columns of a token tile, 128 at most: more tokens share a tile's weights (us, 128
+  // columns / 64: 48 x 6144 x 6144 11.2 / 11.7, 512 x 6144 x 2048 19.3 / 23.3; 64 / 32: 32
+  // x 6144 x 6144 9.3 / 11.0).  With 16 the product's kernel splits the tokens itself,
+  // above them a kernel before it does; 5 to 8 tokens pay for that kernel from about 8
+  // units a CTA (us, 32 / 16: 8 x 40003 x 6144 25.4 / 28.8, 8 x 12288 x 6144 11.0 / 11.8,
+  // 8 x 6144 x 6144 7.9 / 7.8, 7 x 4099 x 2912 6.1 / 5.0).
+  const bool many = (int64_t)p->RT * p->KU > 8 * kMaxGrid;
+  p->nc = s.M <= 4 || (s.M <= 8 && !many) ? 16 : s.M <= 16 ? 32 : s.M <= 32 ? 64 : 128;
   p->mt = p->nc / 2;
   p->TT = (s.M + p->mt - 1) / p->mt;
   p->units = (int64_t)p->RT * p->TT * p->KU;

@@ -1,5 +1,5 @@
 // linear.cu -- y = x W^T (+ bias) for few tokens: MXFP4 weights, bf16
-// activations, fp32 sums, one launch (two above 8 tokens).
+// activations, fp32 sums, one launch (two above 8 tokens, and on large weights above 4).
 //
 // Bound: the weights' bytes (1 x 40003 x 6144: 22.4 us, 5.8 TB/s; 4 x 12288 x 6144:
 // 9.9 us, 4.0 TB/s), behind some 3 us of start, parts and end; from about 32
@@ -13,7 +13,7 @@
 // first thing that their CTAs finish, and the starting share's last.
 //
 // Roles: one thread streams tiles (TMA) and their scale blocks (bulk copy), a
-// warp for each token splits its K chunks into the operand ring (above 8 tokens
+// warp for each token splits its K chunks into the operand ring (with two launches
 // k_split_x does it before, and the stream brings them), one thread issues the
 // MMAs, four warps for every 8 tokens (16 of the largest tile) read the sums out
 // of TMEM.

@@ -76,7 +76,8 @@ def _run(M, N, K, out_type, bias=None, mat=None, x=None, ws=None):
 
 SIZES = [(1, 1, 32), (1, 128, 128), (3, 127, 96), (1, 129, 160), (2, 300, 288), (8, 512, 512), (9, 256, 384),
          (16, 1000, 2912), (17, 64, 32), (31, 130, 416), (32, 512, 1024), (33, 129, 320), (64, 384, 512), (65, 257, 512),
-         (128, 128, 256), (200, 100, 2080), (1000, 300, 96), (3, 60, 40000), (40, 130, 32800), (2, 100003, 64), (1, 6144, 6144), (5, 4099, 2912), (40, 2000, 4096), (1, 20011, 512)]
+         (128, 128, 256), (200, 100, 2080), (1000, 300, 96), (3, 60, 40000), (40, 130, 32800), (2, 100003, 64), (1, 6144, 6144), (5, 4099, 2912), (40, 2000, 4096), (1, 20011, 512), (5, 152001, 96),
+         (8, 3200, 12320)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
