@@ -419,7 +419,9 @@ MOE_API int moe_layer_w4_workspace_size(const moe_layer_shape_t* shape, size_t* 
  * within range).  The workspace is zero-filled once (moe_workspace_init) and
  * then serves any sequence of moe_layer_w4 calls on one stream, of any shapes
  * it is large enough for; moe_get_status reports a device-side wait that ran
- * out (zero-fill the workspace then).  MOE_TEST_WITHHOLD_FLAG applies.       */
+ * out (zero-fill the workspace then).  MOE_TEST_WITHHOLD_FLAG applies;
+ * MOE_TEST_HOLD_ROUTING_US=n (read once per process) has one CTA of every call
+ * route n microseconds late, which changes no result.                       */
 MOE_API int moe_layer_w4(const moe_layer_shape_t* shape, const moe_layer_weights_t* weights, const void* x, void* out,
                          int32_t* topk_ids, float* topk_w, void* workspace, size_t ws_bytes, void* stream);
 

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 
 #include "host.h"
@@ -85,6 +86,16 @@ static int layer_plan(const moe_layer_shape_t& s, LayerPlan* p) {
   p->o_msf = take(tiles * 512);
   p->total = o;
   return MOE_OK;
+}
+
+// Test knob MOE_TEST_HOLD_ROUTING_US=n: one CTA of every moe_layer_w4 call routes
+// n microseconds late (at most a tenth of a second).  Read once per process.
+static uint64_t routing_hold_ns() {
+  static const uint64_t v = [] {
+    const char* e = std::getenv("MOE_TEST_HOLD_ROUTING_US");
+    return static_cast<uint64_t>(std::min(std::max(e ? std::atol(e) : 0l, 0l), 100000l)) * 1000;
+  }();
+  return v;
 }
 
 // Tensor map of `batch` 4-bit matrices [rows][K], boxes of 128 x 128 (tiles land unpacked).
@@ -242,6 +253,7 @@ int moe_layer_w4(const moe_layer_shape_t* shape, const moe_layer_weights_t* w, c
   p.scale = shape->routed_scale; p.eps = shape->norm_eps;
   p.test_withhold = take_withhold();
   p.timeout_ns = wait_timeout_ns();
+  p.test_hold_ns = routing_hold_ns();
   const cudaError_t e = launch_layer_w4(m, p, std::min(sm_count(dev), kMaxGrid), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "moe_layer_w4 kernel launch", e);
 }

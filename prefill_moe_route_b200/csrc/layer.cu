@@ -172,7 +172,7 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
   have(wr); have(x0); have(x1);
   pdl_wait();
   if (blockIdx.x + 1 == gridDim.x) {   // before any block of k_layer_experts can start
-    if (threadIdx.x == 0) { p.sync[0] = 0; p.sync[1] = 0; __threadfence(); }
+    if (threadIdx.x == 0) { p.sync[0] = 0; p.sync[1] = 0; p.sync[2] = 0; __threadfence(); }
     __syncthreads();
   }
   pdl_launch_dependents();
@@ -386,6 +386,10 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
   auto fail = [&](uint32_t site) { wait_ran_out(p.status, abort_flag, 9u << 24 | site << 20); };
   int ticket = 0;
   if (threadIdx.x == 0) ticket = atomicAdd(p.sync, 1);   // in flight while routing runs
+  if (p.test_hold_ns && blockIdx.x + 1 == gridDim.x) {   // test knob: a CTA that routes late
+    const uint64_t until = globaltimer() + p.test_hold_ns;
+    while (globaltimer() < until) { }
+  }
   if (warp < M) {   // one token a warp: there are at least M warps
     float* scratch = reinterpret_cast<float*>(abuf) + warp * kMaxE;   // in the idle ring
     int* ids = S.ids + warp * topk;
@@ -461,6 +465,17 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
       }
   };
 
+  // The sigmoids are empty again for the next call once no CTA can still look for
+  // them: each counts itself behind its routing (a ticket would not do, the first is
+  // drawn before it and may be past the tasks), and the last one empties them.
+  auto routed = [&]() {   // a warp
+    int n = 0;
+    if (lane == 0) n = add_acq_rel_gpu(p.sync + 2, 1);
+    if (__shfl_sync(0xFFFFFFFFu, n, 0) != G - 1) return;
+    for (int i = lane; i < M * E; i += 32) __stcg(p.sig + i, 0u);
+    if (lane < M) __stcg(p.rstd + lane, 0u);
+  };
+
   if (warp == 0) {
     // ------------------------------------------------ weights and their scales
     if (lane == 0) {
@@ -513,12 +528,6 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
       if (!ok) drain();
     }
     __syncwarp();
-    // Every CTA draws one ticket past the tasks.  Whoever draws the last of these
-    // knows that all have routed, and empties what they routed from.
-    if (__shfl_sync(0xFFFFFFFFu, ticket, 0) == sh1.n + sh2.n + G - 1) {
-      for (int i = lane; i < M * E; i += 32) __stcg(p.sig + i, 0u);
-      if (lane < M) __stcg(p.rstd + lane, 0u);
-    }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (the whole warp, one lane issues)
     constexpr uint32_t IDESC = idesc_block_scaled(FMT8_E2M1, FMT8_E4M3, NC);
@@ -587,7 +596,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     uint32_t ph = 0;
     bool ok = true, mid_ready = WORDS;
     Task k;
-    if (WORDS && warp == 3) choices_out();
+    if (WORDS && warp == 3) { routed(); choices_out(); }
     pdl_wait();   // the tokens' columns are there: a kernel's end orders its stores before bulk copies too
     for (int n = 0; ok && (ok = next_task(n, &k)); ++n) {
       if constexpr (WORDS) {
@@ -698,6 +707,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     if (*abort_flag) drain();
     __syncwarp();
   } else if (warp == 3) {
+    routed();
     choices_out();
   } else {
     // ------------------------------------------------ sums
