@@ -70,6 +70,26 @@ constexpr int smem_bytes() {
   return Cfg<NC, SW>::STAGES * Cfg<NC, SW>::STAGE + (int)sizeof(Smem) + 1024;
 }
 
+// Limit of one wait.  Its clock starts when the wait has been polled for a while,
+// not with the kernel: a large call takes longer than a wait may, and the blocks of
+// one can be resident long before the kernel in front of them ends.
+struct Limit {
+  uint64_t until = 0;
+  __device__ __forceinline__ bool over(uint64_t timeout_ns) {
+    const uint64_t now = globaltimer();
+    if (until == 0) until = now + timeout_ns;
+    return now > until;
+  }
+};
+// Bounded wait: false once the limit has passed or another role of the CTA has given up.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag) {
+  uint32_t spins = 0;
+  Limit limit;
+  while (!mbar_try_wait(bar, parity))
+    if ((++spins & 255u) == 0 && (*abort_flag || limit.over(timeout_ns))) return false;
+  return true;
+}
+
 // 8 values of a token's K chunk: 8 bf16 in, 8 bytes of both operand columns (n, n
 // + mt) out; four neighbouring lanes hold a block of 32.
 __device__ __forceinline__ void split_item(const uint4& u, uint8_t* tile, uint8_t* sf, int n, int mt, int g8) {
@@ -151,7 +171,6 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
   // call otherwise); k_split_x waits for the kernel before the call first.
   pdl_launch_dependents();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, S.tmem, 0);
-  const uint64_t deadline = globaltimer() + p.timeout_ns;
   auto fail = [&](uint32_t site) { wait_ran_out(p.status, abort_flag, 8u << 24 | site << 20); };
   auto drain = [&]() { const uint64_t until = globaltimer() + 2000000ull; while (globaltimer() < until) { } };
 
@@ -184,7 +203,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
       have(rt); have(tt); have(ku);
       pdl_wait();
       for (int i = 0; i < nu; ++i) {
-        if (!mbar_wait(&S.empty[st], ph ^ 1, deadline, abort_flag)) { fail(1); ok = false; break; }
+        if (!bar_wait(&S.empty[st], ph ^ 1, p.timeout_ns, abort_flag)) { fail(1); ok = false; break; }
         weights(st, rt, ku);
         if (C::PRE) operand(st, tt, ku);
         if (++st == C::STAGES) { st = 0; ph ^= 1; }
@@ -201,10 +220,11 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
     bool ok = true;
     int ku = u0 % KU;
     bool first = true;
+    pdl_wait();   // nothing to read here, but until the kernel before ends a still ring is no wait of this call
     for (int i = 0; i < nu; ++i) {
       const int b = seg & 1;
-      if (first && !mbar_wait(&S.acce[b], ((seg >> 1) & 1) ^ 1, deadline, abort_flag)) { fail(2); ok = false; break; }
-      if (!mbar_wait(&S.full[st], ph, deadline, abort_flag)) { fail(3); ok = false; break; }
+      if (first && !bar_wait(&S.acce[b], ((seg >> 1) & 1) ^ 1, p.timeout_ns, abort_flag)) { fail(2); ok = false; break; }
+      if (!bar_wait(&S.full[st], ph, p.timeout_ns, abort_flag)) { fail(3); ok = false; break; }
       __syncwarp();
       tc_fence_after();
       const uint32_t d = tmem + b * NC;
@@ -264,7 +284,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
         const int i = i0 + d * ngrp;
         if (i >= nu) break;
         const int st = i % C::STAGES;
-        if (!mbar_wait(&S.empty[st], ((i / C::STAGES) & 1) ^ 1, deadline, abort_flag)) { fail(5); ok = false; break; }
+        if (!bar_wait(&S.empty[st], ((i / C::STAGES) & 1) ^ 1, p.timeout_ns, abort_flag)) { fail(5); ok = false; break; }
         __syncwarp();
         split_item(buf[d], bbuf + st * C::B_BYTES + kk * C::B_TILE, bsf + st * C::SF_BYTES + kk * SF_BLOCK, t, MT, g8);
         fence_proxy_async_smem();
@@ -308,7 +328,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
         }
       };
       if (g0 < m) peek(share + 1, g0);   // most are there before this share's own sum is
-      if (!mbar_wait(&S.accf[b], (seg >> 1) & 1, deadline, abort_flag)) { fail(7); break; }
+      if (!bar_wait(&S.accf[b], (seg >> 1) & 1, p.timeout_ns, abort_flag)) { fail(7); break; }
       __syncwarp();
       tc_fence_after();
 #pragma unroll 1
@@ -330,6 +350,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
           continue;
         }
         uint32_t spins = 0;
+        Limit limit;
 #pragma unroll 1
         for (int cb = share + 1; cb <= c1;) {   // the later shares' parts, in K order
           bool all = true;
@@ -350,7 +371,8 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
             }
             cb += CB;
             if (cb > c1) break;
-          } else if ((++spins & 15u) == 0 && (*abort_flag || globaltimer() > deadline)) {
+            limit = Limit();
+          } else if ((++spins & 15u) == 0 && (*abort_flag || limit.over(p.timeout_ns))) {
             fail(8);
             ok = false;
             break;

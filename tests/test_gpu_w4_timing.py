@@ -79,3 +79,76 @@ def test_beside_a_stream_that_fills_the_gpu(M, shape):
             assert moe.moe_get_status(ws[0]) == (moe.MOE_OK, 0)
             assert all(torch.equal(p, q) for p, q in zip(got, w))
     torch.cuda.synchronize()
+
+
+SLOW_PREDECESSOR = """
+import torch
+import test_gpu_linear_w4 as tl
+import test_gpu_layer_w4 as ty
+import prefill_moe_route_b200 as moe
+# holds its stream 50 ms and lets its successors start at once
+spin = torch.cuda._compile_kernel('''
+extern "C" __global__ void spin(long long ns) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  long long t0, t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  for (int i = 0; i < 100000000; ++i) {
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    if (t - t0 > ns) break;
+  }
+}''', 'spin')
+M = int(sys.argv[1])
+mat = tl.Matrix(1000, 1024)
+sh = moe.MoeLinearShape.of(M, 1000, 1024, out_type=moe.MOE_OUT_F32)
+ws, n = tl._workspace(sh)
+x, out = tl._x(M, 1024), torch.empty(M, 1000, device='cuda')
+L = ty.Layer(512, 8, 2, 256)
+lws = L.workspace()
+for turn in range(2):
+    torch.cuda.synchronize()
+    spin((1, 1, 1), (32, 1, 1), (50000000,))
+    moe.moe_linear_w4(sh, x, mat.packed, None, out, ws, n)
+    assert moe.moe_get_status(ws) == (moe.MOE_OK, 0), turn
+    tl._check(out, x, mat)
+    if M <= 16:
+        y = L.x(M, seed=turn)
+        torch.cuda.synchronize()
+        spin((1, 1, 1), (32, 1, 1), (50000000,))
+        got = L.run(y, lws)
+        assert moe.moe_get_status(lws[0]) == (moe.MOE_OK, 0), turn
+        L.check(y, got)
+print('child ok')
+"""
+
+
+@pytest.mark.parametrize("M", [2, 8, 16, 32, 70])
+def test_a_slow_kernel_before_the_call_is_not_a_wait_of_the_call(M):
+    """The kernel before takes ten times a wait's limit and lets the call's kernels start beside it."""
+    _child(SLOW_PREDECESSOR, M, MOE_WAIT_TIMEOUT_MS="5")
+
+
+LONG_LINEAR = """
+import torch
+import test_gpu_linear_w4 as tl
+import prefill_moe_route_b200 as moe
+M, N, K = 131072, 6144, 6144
+mat = tl.Matrix(N, K)
+x = torch.cat([tl._x(4096, K, seed=i) for i in range(32)])
+sh = moe.MoeLinearShape.of(M, N, K)
+ws, n = tl._workspace(sh)
+out = torch.empty(M, N, device='cuda', dtype=torch.bfloat16)
+for turn in range(2):
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    moe.moe_linear_w4(sh, x, mat.packed, None, out, ws, n)
+    b.record()
+    assert moe.moe_get_status(ws) == (moe.MOE_OK, 0), turn
+    assert a.elapsed_time(b) > 3.0, a.elapsed_time(b)   # several times the limit of a wait
+rows = torch.arange(5, M, 997, device='cuda')
+tl._check(out[rows], x[rows], mat)
+print('child ok')
+"""
+
+
+def test_a_product_may_take_longer_than_a_wait():
+    _child(LONG_LINEAR, MOE_WAIT_TIMEOUT_MS="1")
