@@ -251,7 +251,8 @@ MOE_API int moe_launches_per_call(const moe_shape_t* shape, int device, int* lau
  * error.
  * Device-side waits (the single-launch path's flags between its CTAs) give up
  * after MOE_WAIT_TIMEOUT_MS milliseconds (environment, read once per
- * process; default 2000; moe_linear_w4 counts them for each wait); the kernel then records the first timed-out wait in
+ * process; default 2000; moe_linear_w4 counts them for each wait, moe_layer_w4
+ * from the call's start, with what its weights take on top); the kernel then records the first timed-out wait in
  * status word [2] and returns early instead of trapping.  Test knob:
  * MOE_TEST_WITHHOLD_FLAG=n (read once per process) makes the first n
  * single-launch calls leave one mid flag unpublished, so that those waits run

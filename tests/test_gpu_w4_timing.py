@@ -149,6 +149,29 @@ tl._check(out[rows], x[rows], mat)
 print('child ok')
 """
 
+LONG_LAYER = """
+import torch
+import test_gpu_layer_w4 as ty
+import prefill_moe_route_b200 as moe
+L = ty.Layer(16384, 64, 16, 8192)
+ws = L.workspace()
+x = L.x(int(sys.argv[1]))
+for turn in range(2):
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    got = L.run(x, ws)
+    b.record()
+    assert moe.moe_get_status(ws[0]) == (moe.MOE_OK, 0), turn
+    assert a.elapsed_time(b) > 1.2, a.elapsed_time(b)   # past the limit of a wait
+L.check(x, got)
+print('child ok')
+"""
+
 
 def test_a_product_may_take_longer_than_a_wait():
     _child(LONG_LINEAR, MOE_WAIT_TIMEOUT_MS="1")
+
+
+@pytest.mark.parametrize("M", [4, 8])
+def test_a_layer_may_take_longer_than_a_wait(M):
+    _child(LONG_LAYER, M, MOE_WAIT_TIMEOUT_MS="1")
