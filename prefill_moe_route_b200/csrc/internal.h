@@ -194,7 +194,7 @@ struct LayerParams {
   int32_t* ids_out;         // [M][topk], or null
   float* wts_out;           // [M][topk], or null
   int32_t* status;
-  int32_t* sync;            // [0] next task, [1] pieces of mid tiles stored, [2] CTAs that have routed; k_layer_head zeroes them
+  int32_t* sync;            // [0] next task, [2] CTAs that have routed: zero between calls; [1] pieces of mid tiles stored: k_layer_head zeroes it
   uint32_t *part1, *part2;  // parts of cut tiles: [grid][gate, up of the tokens][128], [grid][tokens][128]; zero between calls
   uint32_t *sig, *rstd;     // sigmoids of the logits [M][E], the norm's factors [M], as parts (zero between calls)
   uint8_t *xop, *xsf;       // the tokens' operand blocks and scale blocks [H/128]

@@ -171,10 +171,10 @@ __global__ void __cluster_dims__(HEAD_SLICES, 1, 1) __launch_bounds__(HEAD_THREA
   }
   have(wr); have(x0); have(x1);
   pdl_wait();
-  if (blockIdx.x + 1 == gridDim.x) {   // before any block of k_layer_experts can start
-    if (threadIdx.x == 0) { p.sync[0] = 0; p.sync[1] = 0; p.sync[2] = 0; __threadfence(); }
-    __syncthreads();
-  }
+  // What k_layer_experts uses before this kernel's end (tickets, the count of routed
+  // CTAs, empty sigmoids) was left ready by the call before, whose kernels have ended;
+  // the count of mid's pieces it uses behind this kernel's end.
+  if (blockIdx.x + 1 == gridDim.x && threadIdx.x == 0) p.sync[1] = 0;
   pdl_launch_dependents();
   if (!logits) {
     if (blockIdx.x - nlogit < H / 128) split_chunk(p, blockIdx.x - nlogit);
@@ -472,6 +472,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
     int n = 0;
     if (lane == 0) n = add_acq_rel_gpu(p.sync + 2, 1);
     if (__shfl_sync(0xFFFFFFFFu, n, 0) != G - 1) return;
+    if (lane == 0) __stcg(p.sync + 2, 0);
     for (int i = lane; i < M * E; i += 32) __stcg(p.sig + i, 0u);
     if (lane < M) __stcg(p.rstd + lane, 0u);
   };
@@ -525,6 +526,8 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
           }
         }
       }
+      // every CTA draws one ticket past the tasks: the last one ends the count
+      if (ticket == sh1.n + sh2.n + G - 1) __stcg(p.sync, 0);
       if (!ok) drain();
     }
     __syncwarp();

@@ -175,3 +175,17 @@ def test_a_product_may_take_longer_than_a_wait():
 @pytest.mark.parametrize("M", [4, 8])
 def test_a_layer_may_take_longer_than_a_wait(M):
     _child(LONG_LAYER, M, MOE_WAIT_TIMEOUT_MS="1")
+
+
+@pytest.mark.parametrize("M", [1, 4, 8, 16])
+@pytest.mark.parametrize("shape", [(512, 8, 2, 256), (2048, 64, 8, 256, 256)])
+def test_a_call_leaves_what_the_next_one_starts_from(M, shape):
+    """The task counter and the count of routed CTAs are zero when a call has ended: the
+    next call's kernels read them before any kernel of that call has ended."""
+    L = Layer(*shape)
+    ws = L.workspace()
+    for turn in range(5):
+        L.run(L.x(M, seed=turn), ws)
+        words = ws[0][:256].view(torch.int32).tolist()
+        assert words[16] == 0 and words[18] == 0 and words[:3] == [0, 0, 0], turn
+    assert moe.moe_get_status(ws[0]) == (moe.MOE_OK, 0)
