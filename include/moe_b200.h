@@ -373,10 +373,12 @@ MOE_API int moe_pack_w4(const uint8_t* q, const uint8_t* scales, int32_t N, int3
 MOE_API int moe_linear_w4_workspace_size(const moe_linear_shape_t* shape, size_t* bytes);
 
 /* The product.  x bf16, 16-byte aligned; w_packed from moe_pack_w4; bias fp32
- * [N] or NULL; out must not overlap an input.  The workspace is zero-filled
- * once (moe_workspace_init) and then serves any sequence of moe_linear_w4
- * calls on one stream, of any shapes it is large enough for; moe_get_status
- * reports a device-side wait that ran out (zero-fill the workspace then).   */
+ * [N] or NULL.  out and the workspace must not overlap another buffer (rows of
+ * out may lie between rows of x, as columns of one buffer do).  The workspace is
+ * zero-filled once (moe_workspace_init) and then serves any sequence of
+ * moe_linear_w4 calls on one stream, of any shapes it is large enough for;
+ * moe_get_status reports a device-side wait that ran out (zero-fill the
+ * workspace then).                                                          */
 MOE_API int moe_linear_w4(const moe_linear_shape_t* shape, const void* x, const void* w_packed, const float* bias,
                           void* out, void* workspace, size_t ws_bytes, void* stream);
 
@@ -413,8 +415,9 @@ typedef struct {
 /* Workspace bytes of moe_layer_w4 (host only, pure; the same for every M).   */
 MOE_API int moe_layer_w4_workspace_size(const moe_layer_shape_t* shape, size_t* bytes);
 
-/* The layer.  x bf16, 16-byte aligned; out bf16 (must not overlap an input);
- * topk_ids int32 [M][topk] and topk_w fp32 [M][topk] out, or NULL.  Weights
+/* The layer.  x bf16, 16-byte aligned; out bf16; topk_ids int32 [M][topk] and
+ * topk_w fp32 [M][topk] out, or NULL.  These and the workspace must not overlap
+ * another buffer (rows of out may lie between rows of x).  Weights
  * 32-byte, scales, norm_w and router_w 16-byte aligned.  A token whose row
  * holds an infinity or a NaN gives NaN (its expert choice is then unspecified,
  * within range).  The workspace is zero-filled once (moe_workspace_init) and

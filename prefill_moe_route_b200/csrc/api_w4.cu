@@ -105,6 +105,41 @@ static bool mx_map(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, 
   return make_map(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, base, d, st, box);
 }
 
+// `rows` rows of `len` bytes, `pitch` bytes apart (rows do not overlap one another).
+struct Span {
+  uintptr_t at;
+  uint64_t rows, len, pitch;
+  uintptr_t end() const { return at + (rows - 1) * pitch + len; }
+};
+static Span span(const void* p, uint64_t bytes) { return {reinterpret_cast<uintptr_t>(p), 1, bytes, bytes}; }
+static Span span(const void* p, uint64_t rows, uint64_t len, uint64_t pitch) { return {reinterpret_cast<uintptr_t>(p), rows, len, pitch}; }
+
+// True if a byte lies in both; null and empty spans overlap nothing.  Rows that lie
+// between the other's rows (columns of one buffer) are apart.
+static bool overlap(const Span& a, const Span& b) {
+  if (!a.at || !b.at || !a.len || !b.len || a.at >= b.end() || b.at >= a.end()) return false;
+  uint64_t i = 0, j = 0;   // only buffers that lie one inside the other get here: row by row
+  if (a.at + a.pitch <= b.at) i = (b.at - a.at) / a.pitch;
+  if (b.at + b.pitch <= a.at) j = (a.at - b.at) / b.pitch;
+  while (i < a.rows && j < b.rows) {
+    const uintptr_t x = a.at + i * a.pitch, y = b.at + j * b.pitch;
+    if (x < y + b.len && y < x + a.len) return true;
+    if (x + a.len <= y) ++i;
+    else ++j;
+  }
+  return false;
+}
+// True if a buffer that the call writes overlaps another or one that it only reads.
+static bool any_overlap(const Span* out, int nout, const Span* in, int nin) {
+  for (int i = 0; i < nout; ++i) {
+    for (int j = i + 1; j < nout; ++j)
+      if (overlap(out[i], out[j])) return true;
+    for (int j = 0; j < nin; ++j)
+      if (overlap(out[i], in[j])) return true;
+  }
+  return false;
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -150,15 +185,20 @@ int moe_linear_w4(const moe_linear_shape_t* shape, const void* x, const void* w_
   if (!aligned(x, 16) || !aligned(w_packed, 256) || !aligned(workspace, 256) || !aligned(bias, 4) ||
       !aligned(out, shape->out_type == MOE_OUT_F32 ? 4 : 2))
     return fail(MOE_ERR_INVALID_ARG, "moe_linear_w4: x needs 16-byte, w_packed and workspace 256-byte, bias and out their type's alignment");
-  if (out == x || out == workspace) return fail(MOE_ERR_INVALID_ARG, "moe_linear_w4: out aliases an input");
+  LinearPlan pl;
+  int rc = linear_plan(*shape, kMaxGrid, &pl);
+  if (rc != MOE_OK) return fail(rc, "moe_linear_w4: unsupported shape");
+  if (ws_bytes < pl.total) return fail(MOE_ERR_WORKSPACE, "moe_linear_w4: workspace smaller than moe_linear_w4_workspace_size");
+  const uint64_t M = shape->M, N = shape->N, K = shape->K, esz = shape->out_type == MOE_OUT_F32 ? 4 : 2;
+  const Span written[2] = {span(out, M, N * esz, shape->ldo * esz), span(workspace, pl.total)};
+  const Span read[3] = {span(x, M, K * 2, shape->ldx * 2), span(w_packed, (uint64_t)pl.RT * pl.KC * 8704), span(bias, N * 4)};
+  if (any_overlap(written, 2, read, 3)) return fail(MOE_ERR_INVALID_ARG, "moe_linear_w4: out or workspace overlaps another buffer");
   const void* ptrs[5] = {x, w_packed, bias, out, workspace};
   const int dev = resolve_device(stream, ptrs, 5);
   if (dev < 0) return dev;
   DeviceGuard g(dev);
-  LinearPlan pl;
-  const int rc = linear_plan(*shape, sm_count(dev), &pl);
+  rc = linear_plan(*shape, sm_count(dev), &pl);
   if (rc != MOE_OK) return fail(rc, "moe_linear_w4: unsupported shape");
-  if (ws_bytes < pl.total) return fail(MOE_ERR_WORKSPACE, "moe_linear_w4: workspace smaller than moe_linear_w4_workspace_size");
   const uint64_t blocks = (uint64_t)pl.RT * pl.KC;
   CUtensorMap map;
   const uint64_t dims[2] = {128, blocks * 128}, strides[1] = {64};
@@ -214,12 +254,16 @@ int moe_layer_w4(const moe_layer_shape_t* shape, const moe_layer_weights_t* w, c
     if (!aligned(ptrs[i], 32)) return fail(MOE_ERR_INVALID_ARG, "moe_layer_w4: weights need 32-byte alignment");
   if (!aligned(workspace, 256) || !aligned(out, 2) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) || !aligned(w->bias, 4))
     return fail(MOE_ERR_INVALID_ARG, "moe_layer_w4: workspace needs 256-byte alignment, out, ids, weights and bias their type's");
-  if (out == x || out == workspace) return fail(MOE_ERR_INVALID_ARG, "moe_layer_w4: out aliases an input");
+  if (ws_bytes < pl.total) return fail(MOE_ERR_WORKSPACE, "moe_layer_w4: workspace smaller than moe_layer_w4_workspace_size");
+  const uint64_t M = shape->M, H = shape->H, I = shape->I, E = shape->E, S = shape->shared_I, choices = M * shape->topk;
+  const Span written[4] = {span(out, M, H * 2, shape->ldo * 2), span(workspace, pl.total), span(topk_ids, choices * 4), span(topk_w, choices * 4)};
+  const Span read[12] = {span(x, M, H * 2, shape->ldx * 2), span(w->norm_w, H * 2), span(w->router_w, E * H * 2), span(w->bias, E * 4),
+                         span(w->w13, E * I * H), span(w->w13_scales, E * I * H / 16), span(w->w2, E * I * H / 2), span(w->w2_scales, E * I * H / 32),
+                         span(sh[0], S * H), span(sh[1], S * H / 16), span(sh[2], S * H / 2), span(sh[3], S * H / 32)};
+  if (any_overlap(written, 4, read, 12)) return fail(MOE_ERR_INVALID_ARG, "moe_layer_w4: a buffer that is written overlaps another");
   const int dev = resolve_device(stream, ptrs, 16);
   if (dev < 0) return dev;
   DeviceGuard g(dev);
-  if (ws_bytes < pl.total) return fail(MOE_ERR_WORKSPACE, "moe_layer_w4: workspace smaller than moe_layer_w4_workspace_size");
-  const uint64_t H = shape->H, I = shape->I, E = shape->E, S = shape->shared_I;
   CUtensorMap m[4];
   bool ok = mx_map(&m[0], w->w13, H, 2 * I, E) && mx_map(&m[1], w->w2, I, H, E);
   if (shared) ok = ok && mx_map(&m[2], sh[0], H, 2 * S, 1) && mx_map(&m[3], sh[2], S, H, 1);

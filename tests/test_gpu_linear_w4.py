@@ -346,3 +346,19 @@ print('child ok')
     env = dict(os.environ, MOE_TEST_WITHHOLD_FLAG="1", MOE_WAIT_TIMEOUT_MS="20")
     r = subprocess.run([sys.executable, "-c", code, str(M)], cwd=ROOT, env=env, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "child ok" in r.stdout, r.stdout[-2000:] + r.stderr[-3000:]
+
+
+@pytest.mark.parametrize("M", [1, 7, 16, 20, 70])
+def test_x_and_out_as_columns_of_one_buffer(M):
+    N, K = 259, 480
+    mat = Matrix(N, K, seed=3)
+    buf = torch.full((M, 768), 77.0, device=DEV, dtype=torch.bfloat16)
+    x, out = buf[:, :K], buf[:, 488:488 + N]
+    x.copy_(_x(M, K))
+    sh = moe.MoeLinearShape.of(M, N, K, ldx=768, ldo=768)
+    ws, n = _workspace(sh)
+    moe.moe_linear_w4(sh, x, mat.packed, None, out, ws, n)
+    _check(out, x, mat)
+    assert bool((buf[:, K:488] == 77.0).all()) and bool((buf[:, 488 + N:] == 77.0).all())
+    over = moe.moe_linear_w4(sh, x, mat.packed, None, buf[:, K - 2:], ws, n, check=False)
+    assert over == moe.MOE_ERR_INVALID_ARG
