@@ -166,8 +166,10 @@ def _ptr(t):
         return None
     try:
         return t.data_ptr()
-    except AttributeError:   # an integer device address
-        return t
+    except AttributeError:
+        if isinstance(t, int):   # a device address
+            return t
+        raise
 
 
 def _current_stream():

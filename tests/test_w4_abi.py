@@ -108,3 +108,14 @@ def test_layer_refuses_pointers_before_any_launch():
                dict(ids=4098), dict(wts=4098)):
         assert call(**kw) == moe.MOE_ERR_INVALID_ARG, kw
     assert moe.load().moe_layer_w4(None, None, None, None, None, None, None, 0, None) == moe.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("bad", [b"\0" * 4096, ctypes.c_void_p(4096), "4096", 4096.0])
+def test_a_buffer_is_a_tensor_or_an_address(bad):
+    """Python objects that ctypes would pass on as host memory are refused by name."""
+    with pytest.raises(AttributeError):
+        moe.moe_linear_w4(_linear(), bad, 8192, None, 16384, 32768, 1 << 30, stream=0)
+    with pytest.raises(AttributeError):
+        moe.moe_round_bf16(bad, 8192, 8, stream=0)
+    with pytest.raises(AttributeError):
+        moe.MoeLayerWeights.of(router_w=bad, w13=1, w13_scales=1, w2=1, w2_scales=1)
