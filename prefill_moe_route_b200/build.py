@@ -14,7 +14,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libmoe_b200.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["route.cu", "gemm.cu", "small.cu", "misc.cu", "probe.cu", "linear.cu", "layer.cu", "api.cu", "api_w4.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "codec.cuh", "w4.cuh", "host.h"]
+HEADERS = ["ptx.cuh", "internal.h", "codec.cuh", "w4.cuh", "w4_params.h", "host.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",

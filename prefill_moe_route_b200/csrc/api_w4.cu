@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "host.h"
+#include "w4_params.h"
 
 namespace moe {
 

@@ -18,12 +18,79 @@
 #pragma once
 #include <atomic>
 
-#include "internal.h"
+#include "w4_params.h"
 #include "ptx.cuh"
 #include "codec.cuh"
 
 namespace moe {
 namespace w4 {
+
+// ------------------------------------------------------------ instructions that only these kernels use
+// Store to a CTA of the cluster that completes 4 bytes of transaction count on a
+// barrier of the same CTA: the value and its arrival in one trip.
+__device__ __forceinline__ void st_async_cluster_f32(uint32_t cluster_saddr, float v, uint32_t cluster_bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(cluster_saddr), "f"(v),
+               "r"(cluster_bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void red_release_gpu(int32_t* p, int32_t v) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ int32_t add_acq_rel_gpu(int32_t* p, int32_t v) {   // the value before
+  int32_t old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
+
+// Has a value worked out by this point of the program (before a wait, say).
+template <typename T>
+__device__ __forceinline__ void have(const T& v) {
+  if constexpr (sizeof(T) == 8) asm volatile("" ::"l"(v) : "memory");
+  else asm volatile("" ::"r"(v) : "memory");
+}
+
+// True in one lane of a converged warp (always the same one).  Tensor-core
+// instructions take their descriptors from uniform registers: issued from a
+// loop that the whole warp runs under this predicate they cost half of what
+// they cost in a loop of one diverged thread (217 against 413 clocks for the
+// copies, four N = 16 MMAs and the commit of one 128 x 128 block).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// TMEM -> registers: this warp's 32 lanes, 1, 2, 4 or 8 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[1]) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+  v[0] = __uint_as_float(r);
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[2]) {
+  uint32_t r[2];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
+  v[0] = __uint_as_float(r[0]);
+  v[1] = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[4]) {
+  uint32_t r[4];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// ------------------------------------------------------------ operands
 
 constexpr int A_TILE = 16384;      // 128 rows x 128 E2M1 in shared memory (8 bytes of codes in each 16)
 constexpr int SF_BLOCK = 512;      // scales of 128 rows x 4 groups, in the tensor cores' order

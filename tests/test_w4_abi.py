@@ -110,7 +110,7 @@ def test_layer_refuses_pointers_before_any_launch():
     assert moe.load().moe_layer_w4(None, None, None, None, None, None, None, 0, None) == moe.MOE_ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("bad", [b"\0" * 4096, ctypes.c_void_p(4096), "4096", 4096.0])
+@pytest.mark.parametrize("bad", [b"\0" * 16, ctypes.c_void_p(4096), "4096", 4096.0], ids=["bytes", "c_void_p", "str", "float"])
 def test_a_buffer_is_a_tensor_or_an_address(bad):
     """Python objects that ctypes would pass on as host memory are refused by name."""
     with pytest.raises(AttributeError):
