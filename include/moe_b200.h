@@ -335,8 +335,10 @@ MOE_API int moe_quantize_fp8_block128(const float* w, int64_t batch, int32_t row
 
 /* ------------------------------------------------------------------------
  * Few-token operators: MXFP4 weights with bf16 activations (nothing but the
- * weights is quantized; the calls above quantize the activations too).  Sums
- * are fp32.  An infinity or a NaN in a token's row makes that token's outputs
+ * weights is quantized; the calls above quantize the activations too).  A bf16
+ * activation counts as it is down to 2^-14 of the largest in its block (32 along
+ * K, from the row's start); a smaller one may be off by 2^-21 of that largest.
+ * Sums are fp32.  An infinity or a NaN in a token's row makes that token's outputs
  * NaN and leaves the other tokens' alone; a subnormal activation (below 2^-126)
  * counts as zero.  Weight scales are finite (code 255 is not looked for).
  * Results do not depend on timing: the same call gives the same bits.
@@ -390,8 +392,9 @@ MOE_API int moe_linear_w4(const moe_linear_shape_t* shape, const void* x, const 
  *            E(h) = (silu(h . gate^T) * (h . up^T)) . down^T
  *   out    = bf16( y (+ x with add_residual) )
  * h is not rounded for the router (fp32 sums, mean(x^2) in fp32 too); for the
- * experts h and the SwiGLU output are held to 2^-9 of each value (h is exact
- * without a norm).
+ * experts h (with a norm) and the routing-weighted SwiGLU output are held to
+ * 2^-9 + 2^-12 of each value, half of bf16's step, or 2^-21 of the largest in its
+ * block of 32 where that is more.  Without a norm h is x, kept as said above.
  * H, I, shared_I multiples of 128 (shared_I 0: no shared expert), E <= 512,
  * topk <= min(E, 16); ldx, ldo: elements between rows (>= H, ldx % 8 == 0).  */
 typedef struct {

@@ -1,0 +1,51 @@
+"""What the few-token operators keep of values far below their block's largest."""
+import pytest
+import torch
+
+import prefill_moe_route_b200 as moe
+from test_gpu_layer_w4 import Layer
+from w4_ref import layer_ref, swiglu_ref, value64
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def _wide(M, H, seed):
+    """Blocks of 32 whose values lie up to 2^24 apart (bf16)."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    x = torch.randn(M, H, generator=g, device=DEV)
+    return (x * torch.exp2(-torch.randint(0, 25, (M, H), generator=g, device=DEV).float())).bfloat16()
+
+
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("M", [1, 4, 8, 16])
+def test_layer_with_blocks_over_many_binades(M, norm):
+    """What two columns keep of h: 2^-9 of each value (and an fp32 value passes through
+    11 bits, 2^-12), but no less than 2^-21 of the block's largest, without a norm that
+    alone: a block's scale leaves its largest between 2^7 and 2^8, lo's finest half step is
+    2^-9 / 32 for values below 2^-6 and 2^-9 of the value above."""
+    L = Layer(512, 16, 4, 256, 128, norm=norm)
+    x = _wide(M, 512, seed=M)
+    ws = L.workspace()
+    out, ids, wts = L.run(x, ws)
+    assert moe.moe_get_status(ws[0]) == (moe.MOE_OK, 0)
+    experts = lambda e: (value64(L.w13[e], L.s13[e]), value64(L.w2[e], L.s2[e]))
+    shared = (value64(L.sh[0][0], L.sh[1][0]), value64(L.sh[2][0], L.sh[3][0]))
+    y, _, _, w, _ = layer_ref(x, L.norm_w, L.eps, L.router_w, L.bias, L.topk, L.scale, experts, shared, L.residual, ids=ids)
+    x0 = x.double()
+    h = x0
+    if norm:
+        h = x0 / torch.sqrt((x0 * x0).mean(-1, keepdim=True) + L.eps) * L.norm_w.double()
+    blk = h.abs().reshape(M, -1, 32).amax(-1).repeat_interleave(32, -1)
+    herr = 2.0 ** -21 * blk + ((2.0 ** -20 + 2.0 ** -12) * h.abs() if norm else 0.0)   # swiglu_ref adds 2^-9 of h
+    tol = torch.zeros_like(y)
+    for e in sorted(set(ids.flatten().tolist())):
+        t, j = (ids == e).nonzero(as_tuple=True)
+        ye, ee = swiglu_ref(h[t], herr[t], *experts(e))
+        tol[t] += w[t, j, None] * (ee + 2.0 ** -16 * ye.abs())
+    tol += swiglu_ref(h, herr, *shared)[1] + 2.0 ** -20 * y.abs() + 2.0 ** -8 * y.abs()
+    assert bool(((wts.double() - w).abs() <= 1e-5 * w.abs() + 1e-7).all())
+    assert bool(((out.double() - y).abs() <= tol).all())
+    assert float((out.double() - y).norm()) <= 2.0 ** -8 * float(y.norm())
