@@ -367,7 +367,8 @@ MOE_API int moe_w4_packed_size(int32_t N, int32_t K, size_t* bytes);
  * into moe_linear_w4's layout, once, offline: blocks of 128 rows x 128 K, a
  * block's codes (8192 bytes, rows of 64) contiguous, [ceil(N/128)][ceil(K/128)]
  * of them, followed by as many 512-byte scale blocks in the order of
- * moe_pack_mxfp4_scales; missing rows and columns are zero.  q 16-byte,
+ * moe_pack_mxfp4_scales; missing rows and columns have zero codes and scale 127
+ * (one).  q 16-byte,
  * packed 256-byte aligned, packed of moe_w4_packed_size bytes, no overlap.  */
 MOE_API int moe_pack_w4(const uint8_t* q, const uint8_t* scales, int32_t N, int32_t K, uint8_t* packed, void* stream);
 

@@ -1,14 +1,38 @@
-"""What the few-token operators keep of values far below their block's largest."""
+"""The few-token operators' layouts, and what they keep of values far below their block's largest."""
 import pytest
 import torch
 
 import prefill_moe_route_b200 as moe
 from test_gpu_layer_w4 import Layer
-from w4_ref import layer_ref, swiglu_ref, value64
+from w4_ref import layer_ref, rand_mx, swiglu_ref, value64
 
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda"
+
+
+def _pack_expected(codes, scales):
+    """The packed matrix byte by byte: absent rows and columns have zero codes and scale 127."""
+    N, K = codes.shape[0], codes.shape[1] * 2
+    RT, KC = -(-N // 128), -(-K // 128)
+    c = torch.zeros(RT * 128, KC * 64, dtype=torch.uint8)
+    c[:N, :K // 2] = codes
+    s = torch.full((RT * 128, KC * 4), 127, dtype=torch.uint8)
+    s[:N, :K // 32] = scales
+    c = c.view(RT, 128, KC, 64).permute(0, 2, 1, 3)                       # [row tile][chunk][row][byte]
+    s = s.view(RT, 4, 32, KC, 4).permute(0, 3, 2, 1, 4)                   # [row tile][chunk][r % 32][r / 32][group]
+    return torch.cat([c.reshape(-1), s.reshape(-1)])
+
+
+@pytest.mark.parametrize("N,K", [(1, 32), (128, 128), (130, 160), (127, 96), (257, 352), (300, 1024)])
+def test_the_packed_layout_is_whole(N, K):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(N + K)
+    codes, scales = rand_mx(g, N, K, lo=0, hi=255)
+    n = moe.moe_w4_packed_size(N, K)
+    packed = torch.full((n,), 0xEE, device=DEV, dtype=torch.uint8)
+    moe.moe_pack_w4(codes, scales, N, K, packed)
+    assert torch.equal(packed.cpu(), _pack_expected(codes.cpu(), scales.cpu()))
 
 
 def _wide(M, H, seed):
