@@ -32,7 +32,7 @@ struct LinearParams {
   const float* bias;        // may be null
   const uint8_t* wcodes;    // packed weights, 8192-byte blocks [N/128][K/128]
   const uint8_t* wsf;       // packed weight scales: 512-byte blocks [N/128][K/128]
-  uint8_t* xop;             // above 8 tokens: operand blocks and scale blocks [token tile][K/128]
+  uint8_t* xop;             // from 9 tokens on, on large weights from 5: operand blocks and scale blocks [token tile][K/128]
   uint8_t* xsf;
   void* out;                // rows ldo elements apart
   uint32_t* part;           // [grid][tokens per tile][128] parts of tiles cut between shares, zero between calls

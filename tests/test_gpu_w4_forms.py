@@ -1,9 +1,12 @@
-"""The few-token operators' layouts, and what they keep of values far below their block's largest."""
+"""The few-token operators' layouts, ranges within a block, and the kernel that 5 to 8 tokens
+take on large weights."""
 import pytest
 import torch
 
 import prefill_moe_route_b200 as moe
 from test_gpu_layer_w4 import Layer
+from test_gpu_linear_w4 import Matrix, _check, _run_raw, _workspace, _x
+from test_gpu_w4_timing import _child
 from w4_ref import layer_ref, rand_mx, swiglu_ref, value64
 
 pytestmark = pytest.mark.gpu
@@ -73,3 +76,95 @@ def test_layer_with_blocks_over_many_binades(M, norm):
     assert bool(((wts.double() - w).abs() <= 1e-5 * w.abs() + 1e-7).all())
     assert bool(((out.double() - y).abs() <= tol).all())
     assert float((out.double() - y).norm()) <= 2.0 ** -8 * float(y.norm())
+
+
+# More than 8 units of 128 x 256 a CTA: there 5 to 8 tokens have their split made by a kernel before.
+LARGE = [(152001, 96), (3200, 12320)]
+
+
+@pytest.fixture(scope="module", params=LARGE, ids=["152001x96", "3200x12320"])
+def large(request):
+    return Matrix(*request.param, seed=11)
+
+
+@pytest.mark.parametrize("M", [5, 8])
+def test_large_weights_a_token_that_is_not_finite_is_nan_alone(M, large):
+    clean = _x(M, large.K, seed=8)
+    want = _run_raw(clean, large)
+    _check(want, clean, large)
+    for v in (float("inf"), float("-inf"), float("nan")):
+        x = clean.clone()
+        x[M // 2, 50] = v
+        got = _run_raw(x, large)
+        assert bool(got[M // 2].isnan().all())
+        keep = torch.arange(M, device=DEV) != M // 2
+        assert torch.equal(got[keep], want[keep])
+
+
+@pytest.mark.parametrize("M", [5, 8])
+def test_large_weights_rows_inside_larger_buffers(M, large):
+    N, K = large.N, large.K
+    xb = torch.full((M + 2, K + 40), float("nan"), device=DEV, dtype=torch.bfloat16)
+    x = xb[1:M + 1, 8:K + 8]
+    x.copy_(_x(M, K))
+    for dt, ot in ((torch.float32, moe.MOE_OUT_F32), (torch.bfloat16, moe.MOE_OUT_BF16)):
+        ob = torch.full((M + 2, N + 3), 77.0, device=DEV, dtype=dt)
+        out = ob[1:M + 1, 1:N + 1]
+        sh = moe.MoeLinearShape.of(M, N, K, ldx=xb.stride(0), ldo=ob.stride(0), out_type=ot)
+        ws, n = _workspace(sh)
+        moe.moe_linear_w4(sh, x, large.packed, None, out, ws, n)
+        _check(out, x, large)
+        ob[1:M + 1, 1:N + 1] = 77.0
+        assert bool((ob == 77.0).all())
+
+
+@pytest.mark.parametrize("M", [5, 8])
+def test_large_weights_captured_and_replayed_beside_other_counts(M, large):
+    """One workspace for 4, M and 16 tokens in one graph: the operand blocks lie behind the
+    parts, which every count leaves empty."""
+    N, K = large.N, large.K
+    counts = (4, M, 16)
+    shs = [moe.MoeLinearShape.of(m, N, K, out_type=moe.MOE_OUT_F32) for m in counts]
+    ws, n = _workspace(*shs)
+    xs = [_x(m, K) for m in counts]
+    outs = [torch.empty(m, N, device=DEV) for m in counts]
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            for _ in range(2):
+                for sh, x, out in zip(shs, xs, outs):
+                    moe.moe_linear_w4(sh, x, large.packed, None, out, ws, n)
+        for seed in range(3):
+            for m, x, out in zip(counts, xs, outs):
+                x.copy_(_x(m, K, seed=20 + seed + m))
+                out.zero_()
+            g.replay()
+            st.synchronize()
+            for x, out in zip(xs, outs):
+                _check(out, x, large)
+    assert moe.moe_get_status(ws) == (moe.MOE_OK, 0)
+
+
+WITHHELD = """
+import torch
+import test_gpu_linear_w4 as t
+import prefill_moe_route_b200 as moe
+M, N, K = (int(a) for a in sys.argv[1:])
+mat = t.Matrix(N, K)
+sh = moe.MoeLinearShape.of(M, N, K, out_type=moe.MOE_OUT_F32)
+ws, n = t._workspace(sh)
+out = torch.empty(M, N, device='cuda')
+moe.moe_linear_w4(sh, t._x(M, K), mat.packed, None, out, ws, n)
+rc, st = moe.moe_get_status(ws)
+assert rc == moe.MOE_ERR_DEVICE_TIMEOUT and st == 1, (rc, st)
+moe.moe_workspace_init(ws, n)
+t._run(M, N, K, moe.MOE_OUT_F32, mat=mat, ws=(ws, n))
+print('child ok')
+"""
+
+
+@pytest.mark.parametrize("M", [5, 8])
+def test_large_weights_a_part_that_never_comes_ends_in_a_status(M):
+    _child(WITHHELD, M, 3200, 12320, MOE_TEST_WITHHOLD_FLAG="1", MOE_WAIT_TIMEOUT_MS="20")
