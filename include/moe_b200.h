@@ -368,8 +368,8 @@ MOE_API int moe_w4_packed_size(int32_t N, int32_t K, size_t* bytes);
  * block's codes (8192 bytes, rows of 64) contiguous, [ceil(N/128)][ceil(K/128)]
  * of them, followed by as many 512-byte scale blocks in the order of
  * moe_pack_mxfp4_scales; missing rows and columns have zero codes and scale 127
- * (one).  q 16-byte,
- * packed 256-byte aligned, packed of moe_w4_packed_size bytes, no overlap.  */
+ * (one).  q 16-byte, packed 256-byte aligned, packed of moe_w4_packed_size
+ * bytes, no overlap.                                                         */
 MOE_API int moe_pack_w4(const uint8_t* q, const uint8_t* scales, int32_t N, int32_t K, uint8_t* packed, void* stream);
 
 /* Workspace bytes of moe_linear_w4 (host only, pure).                       */
@@ -380,8 +380,9 @@ MOE_API int moe_linear_w4_workspace_size(const moe_linear_shape_t* shape, size_t
  * out may lie between rows of x, as columns of one buffer do).  The workspace is
  * zero-filled once (moe_workspace_init) and then serves any sequence of
  * moe_linear_w4 calls on one stream, of any shapes it is large enough for;
- * moe_get_status reports a device-side wait that ran out (zero-fill the
- * workspace then).                                                          */
+ * moe_get_status reports a device-side wait that ran out; zero-fill the
+ * workspace then: until that, every further call on it is reported the same way
+ * and its results are not to be used.                                       */
 MOE_API int moe_linear_w4(const moe_linear_shape_t* shape, const void* x, const void* w_packed, const float* bias,
                           void* out, void* workspace, size_t ws_bytes, void* stream);
 
@@ -421,15 +422,16 @@ MOE_API int moe_layer_w4_workspace_size(const moe_layer_shape_t* shape, size_t* 
 
 /* The layer.  x bf16, 16-byte aligned; out bf16; topk_ids int32 [M][topk] and
  * topk_w fp32 [M][topk] out, or NULL.  These and the workspace must not overlap
- * another buffer (rows of out may lie between rows of x).  Weights
- * 32-byte, scales, norm_w and router_w 16-byte aligned.  A token whose row
- * holds an infinity or a NaN gives NaN (its expert choice is then unspecified,
- * within range).  The workspace is zero-filled once (moe_workspace_init) and
+ * another buffer (rows of out may lie between rows of x).  Weights 32-byte,
+ * scales, norm_w and router_w 16-byte aligned.  A token whose row holds an
+ * infinity or a NaN gives NaN (its expert choice is then unspecified, within
+ * range).  The workspace is zero-filled once (moe_workspace_init) and
  * then serves any sequence of moe_layer_w4 calls on one stream, of any shapes
  * it is large enough for; moe_get_status reports a device-side wait that ran
- * out (zero-fill the workspace then).  MOE_TEST_WITHHOLD_FLAG applies;
- * MOE_TEST_HOLD_ROUTING_US=n (read once per process) has one CTA of every call
- * route n microseconds late, which changes no result.                       */
+ * out (zero-fill the workspace then, as for moe_linear_w4).
+ * MOE_TEST_WITHHOLD_FLAG applies; MOE_TEST_HOLD_ROUTING_US=n (read once per
+ * process) has one CTA of every call route n microseconds late, which changes
+ * no result.                                                                 */
 MOE_API int moe_layer_w4(const moe_layer_shape_t* shape, const moe_layer_weights_t* weights, const void* x, void* out,
                          int32_t* topk_ids, float* topk_w, void* workspace, size_t ws_bytes, void* stream);
 

@@ -529,6 +529,7 @@ k_layer_experts(const __grid_constant__ CUtensorMap tmW13, const __grid_constant
       // every CTA draws one ticket past the tasks: the last one ends the count
       if (ticket == sh1.n + sh2.n + G - 1) __stcg(p.sync, 0);
       if (!ok) drain();
+      if (blockIdx.x == 0) report_used_up(p.status);   // here it holds nobody up
     }
     __syncwarp();
   } else if (warp == 1) {

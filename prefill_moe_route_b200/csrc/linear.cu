@@ -210,6 +210,7 @@ k_linear_w4(const __grid_constant__ CUtensorMap tmW, const LinearParams p) {
         next(rt, tt, ku);
       }
       if (!ok) drain();
+      if (blockIdx.x == 0) report_used_up(p.status);   // here it holds nobody up
     }
     __syncwarp();
   } else if (warp == 1) {

@@ -157,11 +157,18 @@ __device__ __forceinline__ uint32_t sf_byte(uint32_t n, uint32_t q) { return 16u
 
 // A wait ran out: recorded in the status words, and the block's other roles are
 // told.  A function of its own keeps it out of the roles' code, which every call
-// fetches anew.
+// fetches anew.  Word 3 stays until the workspace is zero-filled: what a call that
+// gave up leaves there (parts, tickets) is not what the next one starts from.
 static __device__ __noinline__ void wait_ran_out(int32_t* status, volatile int* abort_flag, uint32_t where) {
   *abort_flag = 1;
   atomicOr(status, ST_TIMEOUT);
   atomicCAS(status + 2, 0, static_cast<int>(0x80000000u | where | (blockIdx.x & 0xFFFu)));
+  atomicOr(status + 3, 1);
+}
+// One thread of a call: the workspace of a call that gave up, not zero-filled since,
+// serves no other.  Reported anew, since moe_get_status clears the status word.
+__device__ __forceinline__ void report_used_up(int32_t* status) {
+  if (__ldcg(status + 3)) atomicOr(status, ST_TIMEOUT);
 }
 
 // a / b for 0 <= a < 2^31, b > 0 and a quotient below 2^21 (then the fp32 quotient

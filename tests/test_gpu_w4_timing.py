@@ -189,3 +189,42 @@ def test_a_call_leaves_what_the_next_one_starts_from(M, shape):
         words = ws[0][:256].view(torch.int32).tolist()
         assert words[16] == 0 and words[18] == 0 and words[:3] == [0, 0, 0], turn
     assert moe.moe_get_status(ws[0]) == (moe.MOE_OK, 0)
+
+
+USED_UP = """
+import torch
+import test_gpu_linear_w4 as tl
+import test_gpu_layer_w4 as ty
+import prefill_moe_route_b200 as moe
+op, M = sys.argv[1], int(sys.argv[2])
+if op == 'linear':
+    mat = tl.Matrix(1024, 4096)
+    sh = moe.MoeLinearShape.of(M, 1024, 4096, out_type=moe.MOE_OUT_F32)
+    ws, n = tl._workspace(sh)
+    x, out = tl._x(M, 4096), torch.empty(M, 1024, device='cuda')
+    call = lambda: moe.moe_linear_w4(sh, x, mat.packed, None, out, ws, n)
+    check = lambda: tl._check(out, x, mat)
+else:
+    L = ty.Layer(1024, 16, 4, 256, 128)
+    ws, n = L.workspace()
+    x = L.x(M)
+    got = []
+    call = lambda: got.append(L.run(x, (ws, n)))
+    check = lambda: L.check(x, got[-1])
+call()   # one hand-over of this call is withheld
+assert moe.moe_get_status(ws) == (moe.MOE_ERR_DEVICE_TIMEOUT, 1)
+for turn in range(3):   # the workspace is not what a call starts from: each says so
+    call()
+    assert moe.moe_get_status(ws) == (moe.MOE_ERR_DEVICE_TIMEOUT, 1), turn
+moe.moe_workspace_init(ws, n)
+for turn in range(2):
+    call()
+    assert moe.moe_get_status(ws) == (moe.MOE_OK, 0)
+    check()
+print('child ok')
+"""
+
+
+@pytest.mark.parametrize("op,M", [("linear", 2), ("linear", 16), ("linear", 70), ("layer", 1), ("layer", 4), ("layer", 8), ("layer", 16)])
+def test_a_workspace_that_was_given_up_on_says_so_until_it_is_zero_filled(op, M):
+    _child(USED_UP, op, M, MOE_TEST_WITHHOLD_FLAG="1", MOE_WAIT_TIMEOUT_MS="20")
