@@ -17,8 +17,9 @@
 // Bound: the selected experts' weight bytes, for few tokens the chain of hand-overs
 // between router, routing, GEMM1, mid and GEMM2.  H = 6144, E = 256, top-8: 16
 // tokens with I = 512 take 83 us (66 experts, 4.1 TB/s: GEMM1 streams at 5.7, GEMM2 at
-// 5.2, 8 us lie between), 4 tokens with I = 256 26.4 us (26 experts, 2.7 TB/s), 1
-// token 16.9 us (1.5 TB/s).  Both products are cut into shares of equal bytes (as in
+// 5.2, 8 us lie between), 4 tokens with I = 256 25.8 us (26 experts, 2.7 TB/s), 1
+// token 15.9 us (1.6 TB/s).  All times in this file are those of calls replayed from a
+// CUDA graph; calls made one by one take 0.5 us more.  Both products are cut into shares of equal bytes (as in
 // linear.cu, parts of a cut tile meet in the share that starts it, in K order), one
 // a CTA: twice as many, smaller ones cost more in parts than they balance (16 tokens
 // 85.0 us, 4 tokens 28.6).  Shares are tasks that the CTAs draw from one counter,

@@ -1,9 +1,12 @@
 // linear.cu -- y = x W^T (+ bias) for few tokens: MXFP4 weights, bf16
 // activations, fp32 sums, one launch (two above 8 tokens, and on large weights above 4).
 //
-// Bound: the weights' bytes (1 x 40003 x 6144: 22.4 us, 5.8 TB/s; 4 x 12288 x 6144:
-// 9.9 us, 4.0 TB/s), behind some 3 us of start, parts and end; from about 32
-// tokens the tiles' way in and out of shared memory.  The product runs on the
+// Bound: the weights' bytes (1 x 40003 x 6144: 24.4 us, 5.4 TB/s, in a burst of 24 calls
+// 22.7; 4 x 12288 x 6144: 9.9 us, 4.0 TB/s), behind some 3 us of start, parts and end;
+// from about 32 tokens the tiles' way in and out of shared memory.  All times in this
+// file are those of calls replayed from a CUDA graph, several matrices in turn; calls
+// made one by one take 0.2 to 0.5 us more each, the smallest 4.8 us instead of 2.6 (the
+// host).  The product runs on the
 // tensor cores with the weights on the MMA's M side straight from their packed
 // 4-bit form (no dequantization) and the tokens as 2 columns each (w4.cuh).  The
 // K-chunks of all row tiles are one sequence of units (128 rows x 256 K, 17 KB)
@@ -33,7 +36,7 @@ constexpr int SF_SLOTS = 4;         // TMEM scale slots: per chunk 4 columns of 
 
 // NC: operand columns, two per token.  SW: warps that split the tokens' K chunks
 // in the kernel; 0: k_split_x has done it before.  Measured (us, N = K = 6144, 8
-// split warps / 16 / before): 4 tokens 6.9 / 7.4 / 8.1, 8 tokens 7.8 / 7.8 / 8.3 (7 x
+// split warps / 16, a variant that is not kept / before): 4 tokens 6.9 / 7.4 / 8.1, 8 tokens 7.8 / 7.8 / 8.3 (7 x
 // 4099 x 2912: 5.2 / 5.6 / 6.1), 16 tokens - / 9.2 / 8.2 (N = 12288: - / 13.4 / 11.4).
 template <int NC, int SW>
 struct Cfg {
