@@ -382,7 +382,8 @@ MOE_API int moe_linear_w4_workspace_size(const moe_linear_shape_t* shape, size_t
  * moe_linear_w4 calls on one stream, of any shapes it is large enough for;
  * moe_get_status reports a device-side wait that ran out; zero-fill the
  * workspace then: until that, every further call on it is reported the same way
- * and its results are not to be used.                                       */
+ * and its results are not to be used.  Another entry point's workspace (that of
+ * moe_layer_w4, say) is another buffer, or zero-filled in between.           */
 MOE_API int moe_linear_w4(const moe_linear_shape_t* shape, const void* x, const void* w_packed, const float* bias,
                           void* out, void* workspace, size_t ws_bytes, void* stream);
 

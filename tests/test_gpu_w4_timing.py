@@ -228,3 +228,58 @@ print('child ok')
 @pytest.mark.parametrize("op,M", [("linear", 2), ("linear", 16), ("linear", 70), ("layer", 1), ("layer", 4), ("layer", 8), ("layer", 16)])
 def test_a_workspace_that_was_given_up_on_says_so_until_it_is_zero_filled(op, M):
     _child(USED_UP, op, M, MOE_TEST_WITHHOLD_FLAG="1", MOE_WAIT_TIMEOUT_MS="20")
+
+
+@pytest.mark.parametrize("M", [1, 4, 8, 16])
+def test_captured_behind_copies_fills_and_joined_streams(M):
+    """The node before a call in a graph is a copy, a fill, or kernels of two streams that
+    meet there; two calls of one graph run side by side."""
+    from test_gpu_linear_w4 import Matrix, _check, _workspace, _x
+    L = Layer(512, 8, 2, 256)
+    mats = [Matrix(512, 512, seed=i, lo=113, hi=116) for i in range(2)]
+    sh = moe.MoeLinearShape.of(M, 512, 512)
+    spaces = [_workspace(sh) for _ in range(2)]
+    lws = L.workspace()
+    src, x, h = (_x(M, 512, seed=i, loud=False) for i in range(3))
+    a, b, y = (torch.empty_like(x) for _ in range(3))
+    ids, wts = torch.empty(M, 2, device=DEV, dtype=torch.int32), torch.empty(M, 2, device=DEV)
+    noise = torch.randn(2048, 2048, device=DEV)
+    lsh = L.shape(M)
+
+    def step(main, side):
+        x.copy_(src)                                                    # a copy node
+        moe.moe_linear_w4(sh, x, mats[0].packed, None, a, *spaces[0])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):                                   # a branch that ends later
+            noise @ noise
+            b.zero_()
+            moe.moe_linear_w4(sh, a, mats[1].packed, None, b, *spaces[1])
+        moe.moe_linear_w4(sh, src, mats[1].packed, None, h, *spaces[0])
+        main.wait_stream(side)
+        moe.moe_layer_w4(lsh, L.weights, b, y, ids, wts, *lws)          # behind both branches
+        a.zero_()                                                       # a fill node
+        moe.moe_linear_w4(sh, y, mats[0].packed, None, a, *spaces[1])
+
+    torch.cuda.synchronize()
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(main):
+        step(main, side)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=main):
+            step(main, side)
+        for turn in range(6):
+            src.copy_(_x(M, 512, seed=50 + turn, loud=False))
+            for t in (x, a, b, y, h):
+                t.fill_(7.0)
+            g.replay()
+            main.synchronize()
+            want = torch.empty_like(x)
+            moe.moe_linear_w4(sh, src, mats[0].packed, None, want, *spaces[0])
+            main.synchronize()
+            _check(b, want, mats[1])
+            _check(h, src, mats[1])
+            L.check(b, (y, ids, wts))
+            _check(a, y, mats[0])
+    for ws in (spaces[0][0], spaces[1][0], lws[0]):
+        assert moe.moe_get_status(ws) == (moe.MOE_OK, 0)
