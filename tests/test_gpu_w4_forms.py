@@ -168,3 +168,49 @@ print('child ok')
 @pytest.mark.parametrize("M", [5, 8])
 def test_large_weights_a_part_that_never_comes_ends_in_a_status(M):
     _child(WITHHELD, M, 3200, 12320, MOE_TEST_WITHHOLD_FLAG="1", MOE_WAIT_TIMEOUT_MS="20")
+
+
+@pytest.mark.parametrize("M", [1, 4, 8, 16])
+@pytest.mark.parametrize("norm,S", [(False, 0), (False, 128), (True, 0)])
+def test_layer_forms_a_token_that_is_not_finite_is_nan_alone(M, norm, S):
+    """Without a norm an infinity gives sigmoids of 0 and 1, so weights of 0 among the chosen;
+    without a shared expert nothing else makes the token NaN."""
+    L = Layer(512, 16, 4, 256, S, norm=norm, residual=False)
+    ws = L.workspace()
+    x = L.x(M)
+    want = L.run(x, ws)
+    bad = M // 2
+    keep = torch.arange(M, device=DEV) != bad
+    for v in (float("nan"), float("inf"), float("-inf")):
+        for sign in (1.0, -1.0):
+            L.router_w[:, 100] = L.router_w[:, 100].abs() * sign   # every logit the same way
+            base = L.run(x, ws)
+            y = x.clone()
+            y[bad, 100] = v
+            out, ids, wts = L.run(y, ws)
+            assert moe.moe_get_status(ws[0]) == (moe.MOE_OK, 0)
+            assert bool(out[bad].isnan().all()) and int(ids.min()) >= 0 and int(ids.max()) < 16
+            assert torch.equal(out[keep], base[0][keep]) and torch.equal(ids[keep], base[1][keep])
+    assert bool(want[0].isfinite().all())
+
+
+@pytest.mark.parametrize("M", [1, 4, 8, 16])
+def test_layer_experts_masked_by_the_bias(M):
+    """A bias of -inf or of fp32's lowest value keeps an expert out while others are left; with
+    fewer left than top-k the masked ones follow, the lower expert first."""
+    L = Layer(512, 16, 4, 256, 128)
+    for low in (float("-inf"), torch.finfo(torch.float32).min):
+        L.bias[:] = 0.1
+        L.bias[3:13] = low
+        ws = L.workspace()
+        x = L.x(M)
+        got = L.run(x, ws)
+        assert moe.moe_get_status(ws[0]) == (moe.MOE_OK, 0)
+        assert not (set(got[1].flatten().tolist()) & set(range(3, 13)))
+        L.check(x, got)
+        L.bias[:] = low
+        L.bias[[5, 9]] = 0.1
+        out, ids, wts = L.run(x, ws)
+        for row in ids.tolist():
+            assert set(row[:2]) == {5, 9} and row[2:] == [0, 1]
+        assert bool(out.isfinite().all())
